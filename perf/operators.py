@@ -1,0 +1,431 @@
+"""Cases of the training-step operators next to the Muon step: causal attention over
+packed sequences (with each head's largest logit) and its backward pass, 8-bit
+activation checkpoints, and the weight-gradient product that reads them.
+
+Every case has a plain form in elementary float32 torch operations and the calls
+that a training program makes of the library.  Head layouts and widths are those
+of the benchmark's workloads (12 and 25 heads of 64, widths 768, 1600 and 6400,
+2048 x 7168 experts) and generic grouped layouts with heads of 128."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+TILE = 32          # a checkpoint block: 32 tokens x 32 columns share one exponent
+E4M3_MAX = 448.0
+
+
+# ------------------------------------------------------------------ the cases
+def listed():
+    """The measured cases; the comment at each says what it stands for."""
+    ragged = [1, 517, 1290, 33, 64, 902, 128, 255, 706, 204]   # 4100 tokens of documents of many lengths
+    return [
+        # The shortest useful call, one prompt on 12 heads of 64: launch latency.
+        dict(name="attention_short", op="attention", lengths="37", heads=12, kv_heads=12, head_dim=64, behind=0),
+        # One packed row of documents on 25 heads of 64 (the 1.5B set's layers), fused q/k/v buffer.
+        dict(name="attention_packed", op="attention", lengths=_text(ragged), heads=25, kv_heads=25, head_dim=64,
+             behind=12),
+        # A long document with grouped heads of 128: bound by matrix products.
+        dict(name="attention_long", op="attention", lengths="8192", heads=32, kv_heads=8, head_dim=128, behind=0),
+        # Three very short documents, backward: latency of the backward's launches.
+        dict(name="backward_short", op="backward", lengths="1,20,43", heads=12, kv_heads=12, head_dim=64, behind=0),
+        # Backward of the packed row.
+        dict(name="backward_packed", op="backward", lengths=_text(ragged), heads=25, kv_heads=25, head_dim=64,
+             behind=12),
+        # Backward of the long document: the largest case of the set.
+        dict(name="backward_long", op="backward", lengths="8192", heads=32, kv_heads=8, head_dim=128, behind=0),
+        # Saving a small layer input and restoring it: latency of the two calls.
+        dict(name="checkpoint_small", op="checkpoint", tokens=77, cols=768, x_type="bf16", pad=0),
+        # Saving and restoring a feed-forward activation of 8192 tokens: bound by memory.
+        dict(name="checkpoint_large", op="checkpoint", tokens=8192, cols=6400, x_type="bf16", pad=0),
+        # Weight gradient of one small square layer from few tokens.
+        dict(name="grad_small", op="grad", tokens=100, cols=256, outs="256", g_type="f32", pad=0),
+        # Gradients of the separate query, key and value projections from one saved input, in one call.
+        dict(name="grad_qkv", op="grad", tokens=8192, cols=1600, outs="1600,1600,1600", g_type="f32", pad=0),
+        # An expert's gradient from the few tokens routed to it, odd in number, kept in bfloat16.
+        dict(name="grad_expert", op="grad", tokens=777, cols=7168, outs="2048", g_type="bf16", pad=0),
+        # A feed-forward layer's gradient over a long batch.
+        dict(name="grad_ffn", op="grad", tokens=16384, cols=1600, outs="6400", g_type="f32", pad=0),
+    ]
+
+
+def _text(numbers):
+    return ",".join(str(n) for n in numbers)
+
+
+def _numbers(text):
+    return [int(t) for t in str(text).split(",") if t != ""]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    """One more case of the same ranges: any head layout, odd lengths and widths."""
+    op = rng.choice(["attention", "backward", "checkpoint", "grad"])
+    if op in ("attention", "backward"):
+        kv = rng.choice([1, 2, 3, 4, 8, 12, 16])
+        heads = kv * rng.choice([g for g in (1, 2, 3, 4, 8) if kv * g <= 32])
+        head_dim = rng.choice([32, 40, 64, 64, 80, 96, 128, 128])
+        total = _log_int(rng, 1, 8192)
+        # what is left is cut into documents until nothing is left
+        lengths, left = [], total
+        while left > 0:
+            n = min(left, _log_int(rng, 1, total))
+            lengths.append(n)
+            left -= n
+            if len(lengths) >= 48:
+                lengths[-1] += left
+                left = 0
+        if rng.random() < 0.3:
+            lengths.insert(rng.randrange(len(lengths) + 1), 0)  # an empty document
+        return dict(op=op, lengths=_text(lengths), heads=heads, kv_heads=kv, head_dim=head_dim,
+                    behind=rng.choice([0, 0, 1, 19]))
+    if op == "checkpoint":
+        tokens, cols = _log_int(rng, 1, 8192), _log_int(rng, 1, 6400)
+        return dict(op=op, tokens=tokens, cols=cols, x_type=rng.choice(["bf16", "f32"]), pad=rng.choice([0, 0, 3, 8]))
+    tokens, cols = _log_int(rng, 1, 16384), _log_int(rng, 16, 6400)
+    outs = []
+    while not outs or (len(outs) < 4 and rng.random() < 0.4):
+        outs.append(_log_int(rng, 16, 6400))
+    # no dearer than the largest listed product
+    budget = 16384 * 1600 * 6400
+    while tokens * cols * sum(outs) > budget:
+        tokens = max(1, tokens // 2)
+    return dict(op=op, tokens=tokens, cols=cols, outs=_text(outs), g_type=rng.choice(["bf16", "f32"]),
+                pad=rng.choice([0, 0, 5, 8]))
+
+
+def work(case):
+    """Bytes and operations of one pass: every input once, every output once."""
+    if case["op"] in ("attention", "backward"):
+        lens = _numbers(case["lengths"])
+        H, K, D = case["heads"], case["kv_heads"], case["head_dim"]
+        T = sum(lens)
+        pairs = sum(n * (n + 1) // 2 for n in lens)
+        q, kv, row = 2 * T * H * D, 2 * T * K * D, 4 * T * H
+        if case["op"] == "attention":
+            return {"bytes": q + 2 * kv + q + row + 4 * H, "flops": 4 * D * H * pairs}
+        # reads q, k, v, o, the upstream gradient and lse; writes dq, dk, dv
+        return {"bytes": 3 * q + 2 * kv + row + q + 2 * kv, "flops": 10 * D * H * pairs}
+    T, C = case["tokens"], case["cols"]
+    blocks = -(-T // TILE) * -(-C // TILE)
+    if case["op"] == "checkpoint":
+        width = 2 if case["x_type"] == "bf16" else 4
+        held = T * C + blocks
+        # the save reads x and writes the checkpoint, the restore reads it and writes the values
+        return {"bytes": width * T * C + 2 * held + 2 * T * C, "flops": 2 * T * C}
+    outs = _numbers(case["outs"])
+    width = 2 if case["g_type"] == "bf16" else 4
+    return {"bytes": T * C + blocks + sum(2 * T * o + width * o * C for o in outs),
+            "flops": sum(2 * T * o * C for o in outs)}
+
+
+# ------------------------------------------------------------------ the inputs
+def _generator(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(int(seed) & 0x7FFFFFFFFFFFFFFF)
+    return g
+
+
+def _normal(shape, gen):
+    return torch.randn(shape, generator=gen, device="cuda", dtype=torch.float32)
+
+
+def _attention_inputs(case, seed):
+    """q, k, v as views of one fused projection output, as a layer has them; heads differ
+    in sharpness, so that some rows attend to few keys."""
+    gen = _generator(seed)
+    lens = _numbers(case["lengths"])
+    H, K, D = case["heads"], case["kv_heads"], case["head_dim"]
+    rows = sum(lens) + case["behind"]
+    fused = _normal((rows, H + 2 * K, D), gen)
+    sharp = 0.5 + 1.5 * torch.rand((1, H, 1), generator=gen, device="cuda")
+    fused[:, :H] *= sharp
+    fused = fused.to(torch.bfloat16)
+    s = dict(lens=lens, q=fused[:, :H], k=fused[:, H:H + K], v=fused[:, H + K:], scale=1.0 / math.sqrt(D))
+    if case["op"] == "backward":
+        s["do"] = (0.02 * _normal((rows, H, D), gen)).to(torch.bfloat16)
+    return s
+
+
+def _activations(tokens, cols, dtype, pad, gen):
+    """Layer inputs: normal, with column scales spread over a factor of ten and a few strong columns."""
+    x = _normal((tokens, cols + pad), gen)
+    spread = torch.exp(0.6 * _normal((1, cols + pad), gen))
+    strong = torch.rand((1, cols + pad), generator=gen, device="cuda") < 0.01
+    x = x * torch.where(strong, 30.0 * spread, spread)
+    return x.to(dtype)[:, :cols]
+
+
+def prepare(case, seed):
+    """What the training program holds before the call."""
+    if case["op"] in ("attention", "backward"):
+        s = _attention_inputs(case, seed)
+        rows, H, _ = s["q"].shape
+        if own:
+            import matrix_muon_step_amd as mm
+            s["packing"] = mm.muon_packing_create(s["lens"])
+        if case["op"] == "attention":
+            # the running maximum of an optimizer step, at its start
+            s["max_logit"] = torch.full((H,), -math.inf, device="cuda", dtype=torch.float32)
+        else:
+            # what the forward pass left
+            s["o"], s["lse"] = _forward_for_backward(s)
+        return dict(case=case, **s)
+    gen = _generator(seed)
+    x = _activations(case["tokens"], case["cols"], TYPES[case.get("x_type", "bf16")], case["pad"], gen)
+    if case["op"] == "checkpoint":
+        return dict(case=case, x=x)
+    dys = [(1e-3 * _normal((case["tokens"], o + case["pad"]), gen)).to(torch.bfloat16)[:, :o]
+           for o in _numbers(case["outs"])]
+    s = dict(case=case, dys=dys)
+    if own:
+        import matrix_muon_step_amd as mm
+        s["saved"] = mm.muon_checkpoint_write([x])[0]
+    else:
+        s["saved"] = _plain_save(x)
+    return s
+
+
+def _forward_for_backward(s):
+    """o (bfloat16) and lse (float32) of the forward pass, made the same way on both sides."""
+    o, lse, _ = _plain_attention(s["q"], s["k"], s["v"], s["lens"], s["scale"])
+    rows, H, D = s["q"].shape
+    out = torch.zeros((rows, H, D), device="cuda", dtype=torch.bfloat16)
+    out[:o.shape[0]] = o.to(torch.bfloat16)
+    stat = torch.zeros((H, rows), device="cuda", dtype=torch.float32)
+    stat[:, :lse.shape[1]] = lse
+    return out, stat
+
+
+# ------------------------------------------------------------------ one pass
+def run(state):
+    case = state["case"]
+    T = sum(state["lens"]) if "lens" in state else 0
+    if case["op"] == "attention":
+        if own:
+            import matrix_muon_step_amd as mm
+            o, lse = mm.muon_attention(state["q"], state["k"], state["v"], state["packing"], scale=state["scale"],
+                                       max_logit=state["max_logit"])
+            return dict(o=o[:T], lse=lse[:, :T], max_logit=state["max_logit"])
+        o, lse, top = _plain_attention(state["q"], state["k"], state["v"], state["lens"], state["scale"])
+        return dict(o=o.to(torch.bfloat16), lse=lse, max_logit=torch.maximum(state["max_logit"], top))
+    if case["op"] == "backward":
+        if own:
+            import matrix_muon_step_amd as mm
+            dq, dk, dv = mm.muon_attention_backward(state["do"], state["q"], state["k"], state["v"], state["o"],
+                                                    state["lse"], state["packing"], scale=state["scale"])
+            return dict(dq=dq[:T], dk=dk[:T], dv=dv[:T])
+        return _plain_backward(state)
+    if case["op"] == "checkpoint":
+        if own:
+            import matrix_muon_step_amd as mm
+            saved = mm.muon_checkpoint_write([state["x"]])
+            return mm.muon_checkpoint_read(saved)[0]
+        return _plain_restore(_plain_save(state["x"])).to(torch.bfloat16)
+    dtype = TYPES[case["g_type"]]
+    if own:
+        import matrix_muon_step_amd as mm
+        grads = [torch.empty((dy.shape[1], case["cols"]), device="cuda", dtype=dtype) for dy in state["dys"]]
+        mm.muon_checkpoint_grad([(dy, state["saved"], g) for dy, g in zip(state["dys"], grads)])
+        return grads
+    x = _plain_restore(state["saved"])
+    return [(dy.float().t().contiguous() @ x).to(dtype) for dy in state["dys"]]
+
+
+# ------------------------------------------------------------------ plain forms
+def _heads_of(t, a, b, group):
+    """Rows a..b of a (tokens, heads, dim) tensor as float32 (heads, rows, dim), each head `group` times."""
+    x = t[a:b].float().permute(1, 0, 2).contiguous()
+    return x if group == 1 else x.repeat_interleave(group, dim=0)
+
+
+def _step_heads(n, group):
+    """How many kv heads a plain pass takes at a time: at most 2^29 scores held."""
+    return max(1, (1 << 29) // max(1, n * n * group))
+
+
+def _plain_scores(q, k, scale):
+    n = q.shape[1]
+    s = (q @ k.transpose(1, 2).contiguous()) * scale
+    hidden = torch.ones((n, n), dtype=torch.bool, device=q.device).triu(1)
+    return s.masked_fill(hidden, -math.inf)
+
+
+def _plain_attention(q, k, v, lens, scale):
+    H, K = q.shape[1], k.shape[1]
+    group, D, T = H // K, q.shape[2], sum(lens)
+    o = torch.empty((T, H, D), device=q.device, dtype=torch.float32)
+    lse = torch.empty((H, T), device=q.device, dtype=torch.float32)
+    top = torch.full((H,), -math.inf, device=q.device, dtype=torch.float32)
+    a = 0
+    for n in lens:
+        b = a + n
+        some = _step_heads(n, group)
+        for g0 in range(0, K if n else 0, some):
+            g1 = min(K, g0 + some)
+            hs = slice(g0 * group, g1 * group)
+            s = _plain_scores(_heads_of(q[:, hs], a, b, 1), _heads_of(k[:, g0:g1], a, b, group), scale)
+            m = s.amax(dim=2, keepdim=True)
+            p = torch.exp(s - m)
+            total = p.sum(dim=2, keepdim=True)
+            o[a:b, hs] = ((p / total) @ _heads_of(v[:, g0:g1], a, b, group)).permute(1, 0, 2)
+            lse[hs, a:b] = (m + torch.log(total))[:, :, 0]
+            top[hs] = torch.maximum(top[hs], m.amax(dim=(1, 2)))
+        a = b
+    return o, lse, top
+
+
+def _plain_backward(state):
+    q, k, v, lens, scale = state["q"], state["k"], state["v"], state["lens"], state["scale"]
+    H, K = q.shape[1], k.shape[1]
+    group, D, T = H // K, q.shape[2], sum(lens)
+    dq = torch.empty((T, H, D), device=q.device, dtype=torch.float32)
+    dk = torch.empty((T, K, D), device=q.device, dtype=torch.float32)
+    dv = torch.empty((T, K, D), device=q.device, dtype=torch.float32)
+    a = 0
+    for n in lens:
+        b = a + n
+        some = _step_heads(n, group)
+        for g0 in range(0, K if n else 0, some):
+            g1 = min(K, g0 + some)
+            hs = slice(g0 * group, g1 * group)
+            qh, kh = _heads_of(q[:, hs], a, b, 1), _heads_of(k[:, g0:g1], a, b, group)
+            vh, gh = _heads_of(v[:, g0:g1], a, b, group), _heads_of(state["do"][:, hs], a, b, 1)
+            oh = _heads_of(state["o"][:, hs], a, b, 1)
+            p = torch.exp(_plain_scores(qh, kh, scale) - state["lse"][hs, a:b, None])
+            dp = gh @ vh.transpose(1, 2).contiguous()
+            ds = p * (dp - (gh * oh).sum(dim=2, keepdim=True)) * scale
+            dq[a:b, hs] = (ds @ kh).permute(1, 0, 2)
+            back = ds.transpose(1, 2).contiguous() @ qh
+            dk[a:b, g0:g1] = back.view(g1 - g0, group, n, D).sum(dim=1).permute(1, 0, 2)
+            back = p.transpose(1, 2).contiguous() @ gh
+            dv[a:b, g0:g1] = back.view(g1 - g0, group, n, D).sum(dim=1).permute(1, 0, 2)
+        a = b
+    return dict(dq=dq.to(torch.bfloat16), dk=dk.to(torch.bfloat16), dv=dv.to(torch.bfloat16))
+
+
+def _blocks(x):
+    """(block rows, 32, block columns, 32) view of x, padded with zeros."""
+    T, C = x.shape
+    R, S = -(-T // TILE), -(-C // TILE)
+    full = torch.zeros((R * TILE, S * TILE), device=x.device, dtype=x.dtype)
+    full[:T, :C] = x
+    return full.view(R, TILE, S, TILE)
+
+
+def _plain_save(x):
+    """Codes (as float32 values of the 8-bit type) kept in 8 bits, and one exponent per block."""
+    y = _blocks(x.float())
+    a = torch.where(torch.isfinite(y), y.abs(), torch.zeros_like(y)).amax(dim=(1, 3), keepdim=True)
+    # smallest e with a <= 448 * 2^e:  a = f * 2^n with f in [0.5, 1), and 448 = 0.875 * 2^9
+    f, n = torch.frexp(a)
+    e = torch.where(f > 0.875, n - 8, n - 9).clamp(min=-117)
+    e = torch.where(a == 0, torch.full_like(e, -117), e)
+    z = torch.ldexp(y, -e)
+    # rounding to 4 significant bits, with steps of at least 2^-9
+    _, ez = torch.frexp(z)
+    ez = torch.where(torch.isfinite(z), ez, torch.zeros_like(ez)).clamp(min=-5)
+    codes = torch.ldexp(torch.round(torch.ldexp(z, 4 - ez)), ez - 4)
+    codes = torch.where(torch.isfinite(z), codes, torch.full_like(z, math.nan))
+    return codes.to(torch.float8_e4m3fn), e, x.shape
+
+
+def _plain_restore(saved):
+    codes, e, (T, C) = saved
+    full = torch.ldexp(codes.float(), e)
+    R, _, S, _ = full.shape
+    return full.reshape(R * TILE, S * TILE)[:T, :C].contiguous()
+
+
+# ------------------------------------------------------------------ 64 bits
+def exact(case, seed):
+    """The outputs of run from the definitions, in float64."""
+    if case["op"] in ("attention", "backward"):
+        return _exact_attention(case, seed)
+    gen = _generator(seed)
+    x = _activations(case["tokens"], case["cols"], TYPES[case.get("x_type", "bf16")], case["pad"], gen)
+    if case["op"] == "checkpoint":
+        return _exact_checkpoint(x)
+    dys = [(1e-3 * _normal((case["tokens"], o + case["pad"]), gen)).to(torch.bfloat16)[:, :o]
+           for o in _numbers(case["outs"])]
+    held = _exact_checkpoint(x)
+    return [torch.mm(dy.double().t().contiguous(), held) for dy in dys]
+
+
+def _exact_checkpoint(x):
+    """Nearest value of the 8-bit type (ties to the even code) times the block's power of two."""
+    table = []
+    for code in range(0x7F):
+        exp, man = code >> 3, code & 7
+        table.append(man * 2.0 ** -9 if exp == 0 else (8 + man) * 2.0 ** (exp - 10))
+    table = torch.tensor(table, dtype=torch.float64, device=x.device)
+    middle = (table[1:] + table[:-1]) / 2
+    out = torch.empty(x.shape, dtype=torch.float64, device=x.device)
+    T, C = x.shape
+    for t in range(0, T, TILE):
+        strip = x[t:t + TILE].double()
+        size = torch.where(torch.isfinite(strip), strip.abs(), torch.zeros_like(strip)).amax(dim=0)
+        pad = (-C) % TILE
+        size = torch.cat([size, size.new_zeros(pad)]).view(-1, TILE).amax(dim=1)
+        e = torch.ceil(torch.log2(size.clamp(min=1e-300) / E4M3_MAX))
+        # log2 may be off next to a power of two: settle by comparison
+        e = torch.where(size <= E4M3_MAX * torch.exp2(e - 1), e - 1, e)
+        e = torch.where(size > E4M3_MAX * torch.exp2(e), e + 1, e).clamp(min=-117)
+        unit = torch.exp2(e).repeat_interleave(TILE)[:C]
+        z = (strip / unit).abs()
+        below = torch.bucketize(z, middle, right=False)   # codes whose upper border lies below z
+        tie = (below < middle.numel()) & (z == middle[below.clamp(max=middle.numel() - 1)])
+        below = torch.where(tie & (below % 2 == 1), below + 1, below)
+        value = table[below.clamp(max=table.numel() - 1)]
+        value = torch.where(torch.isfinite(strip), value, torch.full_like(value, math.nan))
+        out[t:t + TILE] = torch.copysign(value, strip) * unit
+    return out
+
+
+def _exact_attention(case, seed):
+    s = _attention_inputs(case, seed)
+    lens, scale = s["lens"], s["scale"]
+    H, K, D = case["heads"], case["kv_heads"], case["head_dim"]
+    group, T = H // K, sum(lens)
+    rows = s["q"].shape[0]
+    if case["op"] == "backward":
+        held_o, held_lse = _forward_for_backward(s)
+        do = s["do"]
+    o = torch.empty((T, H, D), dtype=torch.float64, device="cuda")
+    lse = torch.empty((H, T), dtype=torch.float64, device="cuda")
+    top = torch.full((H,), -math.inf, dtype=torch.float64, device="cuda")
+    dq = torch.zeros((T, H, D), dtype=torch.float64, device="cuda")
+    dk = torch.zeros((T, K, D), dtype=torch.float64, device="cuda")
+    dv = torch.zeros((T, K, D), dtype=torch.float64, device="cuda")
+    begin = np.concatenate([[0], np.cumsum(lens)])
+    for i, n in enumerate(lens):
+        if n == 0:
+            continue
+        span = slice(int(begin[i]), int(begin[i + 1]))
+        later = torch.arange(n, device="cuda")[None, :] > torch.arange(n, device="cuda")[:, None]
+        for h in range(H):
+            q, k, v = (s["q"][span, h].double(), s["k"][span, h // group].double(), s["v"][span, h // group].double())
+            logits = torch.mm(q, k.t().contiguous()).mul_(scale).masked_fill_(later, -math.inf)
+            if case["op"] == "attention":
+                lse[h, span] = torch.logsumexp(logits, dim=1)
+                o[span, h] = torch.mm(torch.exp(logits - lse[h, span][:, None]), v)
+                top[h] = torch.maximum(top[h], logits.max())
+                continue
+            prob = torch.exp(logits.sub_(held_lse[h, span].double()[:, None]))
+            up = do[span, h].double()
+            dot = (up * held_o[span, h].double()).sum(dim=1)
+            dv[span, h // group] += torch.mm(prob.t().contiguous(), up)
+            prob.mul_(torch.mm(up, v.t().contiguous()) - dot[:, None]).mul_(scale)
+            dq[span, h] = torch.mm(prob, k)
+            dk[span, h // group] += torch.mm(prob.t().contiguous(), q)
+    if case["op"] == "attention":
+        return dict(o=o, lse=lse, max_logit=top)
+    return dict(dq=dq, dk=dk, dv=dv)
