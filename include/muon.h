@@ -259,8 +259,8 @@ typedef struct muon_matrix_plan {
 muon_status_t muon_plan_query(const muon_matrix_t* mats, int64_t n, const muon_hparams_t* hp,
                               muon_plan_info_t* info, muon_matrix_plan_t* per_matrix);
 
-/* Stage timing.  When enabled (per process), every launch the library makes
- * is bracketed by HIP events on the stream it is launched on;
+/* Stage timing.  When enabled (per process), every launch of a step is
+ * bracketed by HIP events on the stream it is launched on;
  * muon_profile_read waits for the recorded events, adds their elapsed times
  * per stage to `ms` and the launch counts to `launches` (arrays of
  * MUON_STAGE_COUNT entries, caller-owned host memory), and clears them. */
@@ -318,6 +318,114 @@ typedef struct muon_qk_clip_matrix {
   const float* max_logit;
 } muon_qk_clip_matrix_t;
 muon_status_t muon_qk_clip(const muon_qk_clip_matrix_t* mats, int64_t n, float tau, void* stream);
+
+/* ---------------------------------------------------------------- training-step
+ * operators next to the Muon step: what produces the arguments of muon_step
+ * and muon_qk_clip in a training step.  Attention gives each head's largest
+ * logit (QK-Clip's input); a saved 8-bit activation and the upstream
+ * gradient give a projection's G.
+ *
+ * As for the step calls: host structures are read only during the call,
+ * device memory is the caller's, everything is validated before anything is
+ * enqueued, work is enqueued on `stream` and the call returns without
+ * waiting.  Apart from muon_packing_create the calls may be captured into a
+ * HIP graph.  Results are the same bits in every run. */
+
+/* A packing: sequences of the given lengths laid end to end in the first
+ * sum(lengths) rows of the token dimension.  muon_packing_create checks the
+ * lengths (each >= 0; sum <= MUON_MAX_TOKENS) and writes the kernels' work
+ * list into `table` (DEVICE, muon_packing_bytes bytes, 256-byte aligned)
+ * through `stream`, which it synchronises; the handle may then be used on any
+ * stream of that device, by any number of calls at once.  The caller keeps
+ * `table` alive and untouched until the last call that uses the handle has
+ * finished on the device; muon_packing_destroy frees host memory only and
+ * does not wait.  Zero sequences, and empty ones, are allowed.
+ * muon_packing_bytes returns 0 on invalid lengths. */
+#define MUON_MAX_TOKENS 1073741824
+typedef struct muon_packing_s* muon_packing_t;
+size_t muon_packing_bytes(const int64_t* lengths, int64_t n);
+muon_status_t muon_packing_create(const int64_t* lengths, int64_t n, void* table, size_t table_bytes, void* stream,
+                                  muon_packing_t* out);
+muon_status_t muon_packing_destroy(muon_packing_t packing);
+
+/* A (tokens, heads, head_dim) bfloat16 tensor in DEVICE memory: element
+ * (t, h, d) at data[t * token_stride + h * head_stride + d].  data is 16-byte
+ * aligned, the strides (in elements) are multiples of 8, >= 0 and at most
+ * MUON_MAX_TOKEN_STRIDE (token) so that views into a fused projection output
+ * work as they are.  Tensors that a call writes must not overlap themselves
+ * or any other tensor of the call; interleaved views of one buffer that
+ * share no element are fine. */
+#define MUON_MAX_TOKEN_STRIDE 4194304
+typedef struct muon_heads {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} muon_heads_t;
+
+/* Causal self-attention over a packing.  Row i of a sequence attends to rows
+ * 0..i of the same sequence; query head h uses key and value head
+ * h / (heads / kv_heads):
+ *   s_ij = scale * q_i . k_j,  lse_i = log sum_{j<=i} exp(s_ij),
+ *   o_i = sum_{j<=i} exp(s_ij - lse_i) v_j
+ * Products of bfloat16 with float32 accumulation; softmax in float32; the
+ * unnormalised probabilities are rounded to bfloat16 for the product with v,
+ * o to bfloat16 once.
+ *   q, o       heads query heads; k, v: kv_heads heads; o is written
+ *   lse        heads rows of lse_stride (>= the packing's tokens) float32,
+ *              4-byte aligned, written
+ *   max_logit  NULL, or logit_heads float32 entries, read and written:
+ *              entry g becomes max(entry, s_ij over every visible pair of its
+ *              heads g * heads / logit_heads ...), so that one array collects
+ *              the maximum over the calls of an optimizer step (the caller
+ *              starts it at -infinity).  logit_heads is heads or kv_heads:
+ *              the latter is what muon_qk_clip takes for a grouped layout
+ *              (query projection with head_dim * heads / kv_heads rows per
+ *              entry, key projection with head_dim).  NaN logits give NaN.
+ *   heads      a multiple of kv_heads >= 1, at most MUON_MAX_HEADS
+ *   head_dim   a multiple of 8, 8..128 (others: MUON_ERR_UNSUPPORTED)
+ *   scale      finite, > 0
+ * Rows of o and lse behind the packing's last sequence are left as they
+ * were, and rows of q, k, v there are not read.  Sequences do not mix: a NaN
+ * or infinity in a sequence reaches rows of that sequence only (there it
+ * may reach rows before it too: 0 * NaN is NaN). */
+#define MUON_MAX_HEADS 4096
+typedef struct muon_attention {
+  muon_heads_t q, k, v, o;
+  float* lse;
+  int64_t lse_stride;
+  float* max_logit;
+  int32_t logit_heads;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  float scale;
+} muon_attention_t;
+muon_status_t muon_attention(const muon_attention_t* args, muon_packing_t packing, void* stream);
+
+/* Backward pass of muon_attention: from q, k, v, the forward's o and lse and
+ * the upstream gradient d_o,
+ *   p_ij = exp(s_ij - lse_i),  delta_i = d_o_i . o_i,
+ *   dv_j = sum_i p_ij d_o_i,  ds_ij = p_ij (d_o_i . v_j - delta_i),
+ *   dq_i = scale * sum_j ds_ij k_j,  dk_j = scale * sum_i ds_ij q_i
+ * (dk and dv summed over the query heads of a group), written as bfloat16,
+ * each rounded once from float32; p and ds are rounded to bfloat16 for the
+ * products.  No atomics.  Rows behind the last sequence are left as they
+ * were.  Workspace: DEVICE, 256-byte aligned, muon_attention_backward_workspace_bytes
+ * bytes (0 and muon_last_error() on invalid arguments; data pointers are not
+ * looked at). */
+typedef struct muon_attention_grad {
+  muon_heads_t q, k, v, o, d_o;
+  const float* lse;
+  int64_t lse_stride;
+  muon_heads_t dq, dk, dv;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  float scale;
+} muon_attention_grad_t;
+size_t muon_attention_backward_workspace_bytes(const muon_attention_grad_t* args, muon_packing_t packing);
+muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_packing_t packing, void* workspace,
+                                      size_t workspace_bytes, void* stream);
 
 /* Bandwidth yardstick for the HBM-bound stages (the measurement side of the
  * boundary, not part of a step): copies `bytes` from src to dst (DEVICE

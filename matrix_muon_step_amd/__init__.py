@@ -7,5 +7,6 @@ from .binding import (  # noqa: F401
     muon_step_static, MUON_STATIC_WORKSPACE_BYTES, muon_plan_create, MuonPlan,
     muon_step_diag, diag_records, DIAG_FIELDS,
     muon_orthogonalize_workspace_bytes, muon_orthogonalize, muon_plan_query,
-    muon_profile_enable, muon_profile_read, muon_copy_probe, muon_qk_clip, lib, LIB_PATH,
+    muon_profile_enable, muon_profile_read, muon_copy_probe, muon_qk_clip,
+    MuonPacking, muon_packing_create, muon_attention, muon_attention_backward, lib, LIB_PATH,
 )

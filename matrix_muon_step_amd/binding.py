@@ -112,6 +112,39 @@ class muon_qk_clip_matrix_t(ctypes.Structure):
     ]
 
 
+class muon_heads_t(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+class muon_attention_t(ctypes.Structure):
+    _fields_ = [(n, muon_heads_t) for n in ("q", "k", "v", "o")] + [
+        ("lse", ctypes.c_void_p),
+        ("lse_stride", ctypes.c_int64),
+        ("max_logit", ctypes.c_void_p),
+        ("logit_heads", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class muon_attention_grad_t(ctypes.Structure):
+    _fields_ = [(n, muon_heads_t) for n in ("q", "k", "v", "o", "d_o")] + [
+        ("lse", ctypes.c_void_p),
+        ("lse_stride", ctypes.c_int64),
+    ] + [(n, muon_heads_t) for n in ("dq", "dk", "dv")] + [
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 class MuonError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{muon_status_string(status)}: {message}")
@@ -170,6 +203,20 @@ def lib() -> ctypes.CDLL:
                 L.muon_qk_clip.restype = ctypes.c_int
                 L.muon_qk_clip.argtypes = [P(muon_qk_clip_matrix_t), ctypes.c_int64, ctypes.c_float,
                                            ctypes.c_void_p]
+                L.muon_packing_bytes.restype = ctypes.c_size_t
+                L.muon_packing_bytes.argtypes = [P(ctypes.c_int64), ctypes.c_int64]
+                L.muon_packing_create.restype = ctypes.c_int
+                L.muon_packing_create.argtypes = [P(ctypes.c_int64), ctypes.c_int64, ctypes.c_void_p,
+                                                  ctypes.c_size_t, ctypes.c_void_p, P(ctypes.c_void_p)]
+                L.muon_packing_destroy.restype = ctypes.c_int
+                L.muon_packing_destroy.argtypes = [ctypes.c_void_p]
+                L.muon_attention.restype = ctypes.c_int
+                L.muon_attention.argtypes = [P(muon_attention_t), ctypes.c_void_p, ctypes.c_void_p]
+                L.muon_attention_backward_workspace_bytes.restype = ctypes.c_size_t
+                L.muon_attention_backward_workspace_bytes.argtypes = [P(muon_attention_grad_t), ctypes.c_void_p]
+                L.muon_attention_backward.restype = ctypes.c_int
+                L.muon_attention_backward.argtypes = [P(muon_attention_grad_t), ctypes.c_void_p, ctypes.c_void_p,
+                                                      ctypes.c_size_t, ctypes.c_void_p]
                 L.muon_copy_probe.restype = ctypes.c_int
                 L.muon_copy_probe.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32,
                                               ctypes.c_void_p]
@@ -576,3 +623,189 @@ def muon_qk_clip(matrices, tau: float, stream=None) -> None:
         arr[k] = muon_qk_clip_matrix_t(W.data_ptr(), W.shape[0], W.shape[1], int(head_dim), 0, S.data_ptr())
     with _on(device, stream) as st:
         _check(lib().muon_qk_clip(arr, n, float(tau), ctypes.c_void_p(st.cuda_stream)))
+
+
+# ---------------------------------------------------------------- training-step operators
+class MuonPacking:
+    """Sequences of given lengths laid end to end (muon_packing_create): the
+    work list of muon_attention and muon_attention_backward.  One serves every
+    layer of a batch, forward and backward, on any stream of its device.  Keep
+    it alive as long as a graph that was captured with it is replayed."""
+
+    def __init__(self, handle, lengths, table, device):
+        self._h = handle
+        self._table = table
+        self.lengths = tuple(lengths)
+        self.tokens = sum(lengths)
+        self.device = device
+
+    def _enter(self, device, stream):
+        """The handle for a call on `stream`, after which the table's memory
+        is not handed out again before that stream is done with it."""
+        if not self._h:
+            raise RuntimeError("the packing is closed")
+        if device is not None and device != self.device:
+            raise ValueError(f"the packing is on {self.device}, the call's tensors on {device}")
+        self._table.record_stream(stream)
+        return ctypes.c_void_p(self._h)
+
+    def close(self) -> None:
+        """Frees the handle; calls already enqueued are not disturbed."""
+        if self._h:
+            h, self._h = self._h, None
+            _check(lib().muon_packing_destroy(h))
+            self._table = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # interpreter shutdown
+            pass
+
+
+def muon_packing_create(lengths: Sequence[int], device=None, stream=None) -> MuonPacking:
+    """The packing of sequences of these lengths (host integers >= 0) on
+    `device` (default: the current one).  Waits for `stream`."""
+    import torch
+
+    lengths = [int(n) for n in lengths]
+    arr = (ctypes.c_int64 * max(1, len(lengths)))(*lengths)
+    need = int(lib().muon_packing_bytes(arr, len(lengths)))
+    if need == 0:
+        raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error())
+    device = torch.device("cuda" if device is None else device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with _on(device, stream) as st:
+        table = _alloc_workspace(need, device)
+        h = ctypes.c_void_p()
+        _check(lib().muon_packing_create(arr, len(lengths), ctypes.c_void_p(table.data_ptr()), need,
+                                         ctypes.c_void_p(st.cuda_stream), ctypes.byref(h)))
+    return MuonPacking(h.value, lengths, table, device)
+
+
+def _heads_tensor(name, t, rows, device, like=None):
+    """Checks a (rows, heads, head_dim) bfloat16 tensor; returns its muon_heads_t and the call's device."""
+    import torch
+
+    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a bfloat16 GPU tensor (tokens, heads, head_dim)")
+    device = _same_device(device, t, name)
+    if t.shape[0] != rows:
+        raise ValueError(f"{name} has {t.shape[0]} rows, the call {rows}")
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"{name} must have the shape {tuple(like.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # the stride of a dimension of size one says nothing
+    ts = t.stride(0) if t.shape[0] > 1 else 0
+    hs = t.stride(1) if t.shape[1] > 1 else 0
+    return muon_heads_t(t.data_ptr(), ts, hs), device
+
+
+def _attention_rows(q, k, v, packing):
+    rows = q.shape[0]
+    if rows < packing.tokens:
+        raise ValueError(f"q has {rows} rows, the packing {packing.tokens} tokens")
+    if k.shape != v.shape:
+        raise ValueError("k and v must have one shape")
+    if k.dim() == 3 and q.dim() == 3 and k.shape[2] != q.shape[2]:
+        raise ValueError("q, k and v must have one head_dim")
+    return rows
+
+
+def _lse_tensor(lse, heads, rows, device):
+    import torch
+
+    if not lse.is_cuda or lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape != (heads, rows):
+        raise ValueError("lse must be a float32 GPU tensor (heads, tokens)")
+    if rows > 1 and lse.stride(1) != 1:
+        raise ValueError("lse: the last dimension must be contiguous")
+    return _same_device(device, lse, "lse")
+
+
+def _new_rows(shape, tokens, dim, device, dtype):
+    """An output with zeros in the rows that the call leaves alone (those
+    behind the packing's last sequence)."""
+    import torch
+
+    t = torch.empty(shape, device=device, dtype=dtype)
+    if shape[dim] > tokens:
+        t.narrow(dim, tokens, shape[dim] - tokens).zero_()
+    return t
+
+
+def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, max_logit=None, stream=None):
+    """Causal self-attention of packed sequences; returns (o, lse).
+
+    q is (rows, heads, head_dim), k and v (rows, kv_heads, head_dim), bfloat16,
+    rows >= packing.tokens; views into a fused projection output are taken as
+    they are.  o is bfloat16 like q, lse float32 (heads, rows).  Outputs given
+    by the caller keep what they hold in rows behind the last sequence; outputs
+    made here hold zeros there.  scale defaults to head_dim ** -0.5.
+
+    max_logit: a float32 tensor of heads or kv_heads entries, each raised to
+    the largest scaled logit of its heads in this call: start it at -inf once
+    per optimizer step, pass it to every call of the layer, then hand it to
+    muon_qk_clip (with one entry per key head, the query projection's head_dim
+    there is head_dim * heads // kv_heads)."""
+    import torch
+
+    rows = _attention_rows(q, k, v, packing)
+    dq, device = _heads_tensor("q", q, rows, None)
+    dk, device = _heads_tensor("k", k, rows, device)
+    dv, device = _heads_tensor("v", v, rows, device)
+    heads, kv_heads, head_dim = q.shape[1], k.shape[1], q.shape[2]
+    logit_heads = 0
+    if max_logit is not None:
+        if (not max_logit.is_cuda or max_logit.dtype != torch.float32 or not max_logit.is_contiguous()
+                or max_logit.numel() not in (heads, kv_heads)):
+            raise ValueError("max_logit must be a contiguous float32 GPU tensor of heads or kv_heads entries")
+        device = _same_device(device, max_logit, "max_logit")
+        logit_heads = max_logit.numel()
+    with _on(device, stream) as st:
+        if o is None:
+            o = _new_rows(q.shape, packing.tokens, 0, device, torch.bfloat16)
+        if lse is None:
+            lse = _new_rows((heads, rows), packing.tokens, 1, device, torch.float32)
+        do, device = _heads_tensor("o", o, rows, device, like=q)
+        device = _lse_tensor(lse, heads, rows, device)
+        args = muon_attention_t(dq, dk, dv, do, lse.data_ptr(), lse.stride(0) if heads > 1 else rows,
+                                max_logit.data_ptr() if max_logit is not None else None, logit_heads, heads, kv_heads,
+                                head_dim, float(head_dim ** -0.5 if scale is None else scale))
+        _check(lib().muon_attention(ctypes.byref(args), packing._enter(device, st), ctypes.c_void_p(st.cuda_stream)))
+    return o, lse
+
+
+def muon_attention_backward(do, q, k, v, o, lse, packing: MuonPacking, scale=None, dq=None, dk=None, dv=None,
+                            workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of muon_attention, bfloat16, from the upstream
+    gradient `do` and what the forward call took and returned.  As there,
+    rows behind the last sequence stay as they are in outputs given by the
+    caller and are zero in outputs made here."""
+    import torch
+
+    rows = _attention_rows(q, k, v, packing)
+    device, views = None, {}
+    for name, t, like in (("q", q, None), ("k", k, None), ("v", v, None), ("o", o, q), ("do", do, q)):
+        views[name], device = _heads_tensor(name, t, rows, device, like=like)
+    heads, kv_heads, head_dim = q.shape[1], k.shape[1], q.shape[2]
+    device = _lse_tensor(lse, heads, rows, device)
+    with _on(device, stream) as st:
+        outs = {}
+        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            outs[name] = _new_rows(like.shape, packing.tokens, 0, device, torch.bfloat16) if t is None else t
+            views[name], device = _heads_tensor(name, outs[name], rows, device, like=like)
+        args = muon_attention_grad_t(views["q"], views["k"], views["v"], views["o"], views["do"], lse.data_ptr(),
+                                     lse.stride(0) if heads > 1 else rows, views["dq"], views["dk"], views["dv"], heads,
+                                     kv_heads, head_dim, float(head_dim ** -0.5 if scale is None else scale))
+        handle = packing._enter(device, st)
+        need = int(lib().muon_attention_backward_workspace_bytes(ctypes.byref(args), handle))
+        if need == 0:
+            raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error())
+        if workspace is None:
+            workspace = _alloc_workspace(need, device)
+        ws_ptr, ws_len = _ws_args(workspace, device)
+        _check(lib().muon_attention_backward(ctypes.byref(args), handle, ws_ptr, ws_len,
+                                             ctypes.c_void_p(st.cuda_stream)))
+    return outs["dq"], outs["dk"], outs["dv"]

@@ -10,6 +10,7 @@
 #include <string>
 #include <vector>
 
+#include "api_common.h"
 #include "muon.h"
 #include "muon_internal.h"
 
@@ -22,7 +23,7 @@ using namespace muon;
 // kept in g_scratch_ptr.
 static __device__ __align__(256) unsigned char scratch[MUON_STATIC_WORKSPACE_BYTES];
 
-namespace {
+namespace muon {
 
 thread_local std::string g_last_error;
 
@@ -31,9 +32,36 @@ muon_status_t fail(muon_status_t st, const std::string& msg) {
   return st;
 }
 
-constexpr size_t kAlign = 256;
-size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
-int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+muon_status_t hip_fail(hipError_t e, const char* where) {
+  return fail(MUON_ERR_HIP, std::string("muon: ") + where + ": " + hipGetErrorString(e));
+}
+
+muon_status_t check_aliasing(std::vector<Range>& rs) {
+  std::sort(rs.begin(), rs.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t max_end_any = 0, max_end_w = 0;
+  const Range* last_any = nullptr;
+  const Range* last_w = nullptr;
+  for (const Range& r : rs) {
+    if (r.lo == r.hi) continue;
+    if (r.lo < max_end_w) {
+      return fail(MUON_ERR_ALIAS, std::string("muon: ") + r.what + " of matrix " +
+                                      std::to_string(r.idx) + " overlaps " + last_w->what +
+                                      " of matrix " + std::to_string(last_w->idx));
+    }
+    if (r.writable && r.lo < max_end_any) {
+      return fail(MUON_ERR_ALIAS, std::string("muon: ") + r.what + " of matrix " +
+                                      std::to_string(r.idx) + " overlaps " + last_any->what +
+                                      " of matrix " + std::to_string(last_any->idx));
+    }
+    if (r.hi > max_end_any) { max_end_any = r.hi; last_any = &r; }
+    if (r.writable && r.hi > max_end_w) { max_end_w = r.hi; last_w = &r; }
+  }
+  return MUON_OK;
+}
+
+}  // namespace muon
+
+namespace {
 
 // One matrix as the planner sees it (host side, before pointers are bound).
 struct Item {
@@ -63,38 +91,6 @@ struct Plan {
   std::vector<int64_t> x_offset;
   int ns_steps = 0;
 };
-
-struct Range {
-  uintptr_t lo, hi;
-  bool writable;
-  const char* what;
-  int64_t idx;
-};
-
-muon_status_t check_aliasing(std::vector<Range>& rs) {
-  std::sort(rs.begin(), rs.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-  uintptr_t max_end_any = 0, max_end_w = 0;
-  const Range* last_any = nullptr;
-  const Range* last_w = nullptr;
-  for (const Range& r : rs) {
-    if (r.lo == r.hi) continue;
-    if (r.lo < max_end_w) {
-      return fail(MUON_ERR_ALIAS, std::string("muon: ") + r.what + " of matrix " +
-                                      std::to_string(r.idx) + " overlaps " + last_w->what +
-                                      " of matrix " + std::to_string(last_w->idx));
-    }
-    if (r.writable && r.lo < max_end_any) {
-      return fail(MUON_ERR_ALIAS, std::string("muon: ") + r.what + " of matrix " +
-                                      std::to_string(r.idx) + " overlaps " + last_any->what +
-                                      " of matrix " + std::to_string(last_any->idx));
-    }
-    if (r.hi > max_end_any) { max_end_any = r.hi; last_any = &r; }
-    if (r.writable && r.hi > max_end_w) { max_end_w = r.hi; last_w = &r; }
-  }
-  return MUON_OK;
-}
-
-bool finite(float x) { return isfinite(x); }
 
 // Kernel configurations of one matrix: (symmetric stages, BX stage).
 struct MatCfg {
@@ -479,10 +475,6 @@ XcdSplit make_split(const Plan& plan, int tab, int mode) {
     sp.max_len = std::max(sp.max_len, start[x + 1] - start[x]);
   }
   return sp;
-}
-
-muon_status_t hip_fail(hipError_t e, const char* where) {
-  return fail(MUON_ERR_HIP, std::string("muon: ") + where + ": " + hipGetErrorString(e));
 }
 
 // Launch sequence of one call.  The descriptor table is uploaded into the
