@@ -427,6 +427,68 @@ size_t muon_attention_backward_workspace_bytes(const muon_attention_grad_t* args
 muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_packing_t packing, void* workspace,
                                       size_t workspace_bytes, void* stream);
 
+/* 8-bit activation checkpoints: a layer's input x (tokens x cols, row-major)
+ * kept from the forward to the backward pass in half the bytes of bfloat16.
+ * Blocks of 32 tokens x 32 columns share the exponent e, the smallest integer
+ * >= -117 with max |x| <= 448 * 2^e over the block's finite values; each
+ * value is held as the 8-bit number (4 exponent and 3 mantissa bits, e4m3)
+ * nearest to x * 2^-e, ties to even, and stands for that number times 2^e:
+ * off by at most 2^-4 of x, or by 2^(e-10) where |x| < 2^(e-6).  NaN and
+ * infinities are held as NaN.  A held value is exact in bfloat16.
+ *   x         DEVICE, element (t, c) at x[t * x_stride + c], dtype MUON_F32 or
+ *             MUON_BF16, aligned to its element; x_stride >= cols
+ *   data      DEVICE, 256-byte aligned, muon_checkpoint_bytes(tokens, cols)
+ *             bytes (cols and tokens rounded up to 32, plus 1 / 1024); an
+ *             opaque layout, made for muon_checkpoint_grad
+ *   tokens    >= 0, <= MUON_MAX_TOKENS; cols: 1 .. MUON_MAX_DIM
+ * muon_checkpoint_write fills every item's data from its x;
+ * muon_checkpoint_read writes the held values to x (each exact in bfloat16),
+ * for backward passes that need the input itself.  One launch per 32 items;
+ * buffers that a call writes overlap nothing else of the call. */
+typedef struct muon_checkpoint {
+  void* x;
+  int64_t x_stride;
+  int32_t x_dtype;
+  int32_t reserved;
+  void* data;
+  int64_t tokens;
+  int64_t cols;
+} muon_checkpoint_t;
+size_t muon_checkpoint_bytes(int64_t tokens, int64_t cols); /* 0 on invalid arguments */
+muon_status_t muon_checkpoint_write(const muon_checkpoint_t* items, int64_t n, void* stream);
+muon_status_t muon_checkpoint_read(const muon_checkpoint_t* items, int64_t n, void* stream);
+
+/* Weight gradients from checkpoints, G of muon_step: for a projection y = x W^T
+ * with W outs x cols,
+ *   G[o][c] = sum_t dy[t][o] * x^[t][c]      (accumulate: added to G)
+ * with x^ the checkpoint's held values: exact bfloat16 products, float32
+ * sums, one rounding to G's type.
+ *   dy    DEVICE bfloat16, element (t, o) at dy[t * dy_stride + o], 2-byte
+ *         aligned, dy_stride >= outs and <= MUON_MAX_TOKEN_STRIDE (a 16-byte
+ *         aligned dy with a stride that is a multiple of 8 is read fastest)
+ *   data  a checkpoint of (tokens, cols); matrices of a call may share it
+ *   G     DEVICE, outs x cols row-major, MUON_F32 or MUON_BF16, 16-byte
+ *         aligned, overlapping nothing else of the call
+ *   accumulate  0: G is written; 1: the sum is added to it in float32
+ * All matrices share launches (24 per launch).  tokens == 0 gives zeros
+ * (or leaves G with accumulate).  Workspace: DEVICE, 256-byte aligned,
+ * muon_checkpoint_grad_workspace_bytes bytes; may be 0 (then workspace may
+ * be NULL), which muon_last_error() being empty tells from an error. */
+typedef struct muon_checkpoint_grad {
+  const void* dy;
+  int64_t dy_stride;
+  const void* data;
+  int64_t tokens;
+  int64_t cols;
+  void* G;
+  int64_t outs;
+  int32_t g_dtype;
+  int32_t accumulate;
+} muon_checkpoint_grad_t;
+size_t muon_checkpoint_grad_workspace_bytes(const muon_checkpoint_grad_t* mats, int64_t n);
+muon_status_t muon_checkpoint_grad(const muon_checkpoint_grad_t* mats, int64_t n, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /* Bandwidth yardstick for the HBM-bound stages (the measurement side of the
  * boundary, not part of a step): copies `bytes` from src to dst (DEVICE
  * memory, 16-byte aligned, bytes a multiple of 16, disjoint) with a plain

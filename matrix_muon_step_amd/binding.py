@@ -145,6 +145,32 @@ class muon_attention_grad_t(ctypes.Structure):
     ]
 
 
+class muon_checkpoint_t(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64),
+        ("x_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("data", ctypes.c_void_p),
+        ("tokens", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+    ]
+
+
+class muon_checkpoint_grad_t(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("dy_stride", ctypes.c_int64),
+        ("data", ctypes.c_void_p),
+        ("tokens", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("G", ctypes.c_void_p),
+        ("outs", ctypes.c_int64),
+        ("g_dtype", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32),
+    ]
+
+
 class MuonError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{muon_status_string(status)}: {message}")
@@ -217,6 +243,16 @@ def lib() -> ctypes.CDLL:
                 L.muon_attention_backward.restype = ctypes.c_int
                 L.muon_attention_backward.argtypes = [P(muon_attention_grad_t), ctypes.c_void_p, ctypes.c_void_p,
                                                       ctypes.c_size_t, ctypes.c_void_p]
+                L.muon_checkpoint_bytes.restype = ctypes.c_size_t
+                L.muon_checkpoint_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
+                for f in (L.muon_checkpoint_write, L.muon_checkpoint_read):
+                    f.restype = ctypes.c_int
+                    f.argtypes = [P(muon_checkpoint_t), ctypes.c_int64, ctypes.c_void_p]
+                L.muon_checkpoint_grad_workspace_bytes.restype = ctypes.c_size_t
+                L.muon_checkpoint_grad_workspace_bytes.argtypes = [P(muon_checkpoint_grad_t), ctypes.c_int64]
+                L.muon_checkpoint_grad.restype = ctypes.c_int
+                L.muon_checkpoint_grad.argtypes = [P(muon_checkpoint_grad_t), ctypes.c_int64, ctypes.c_void_p,
+                                                   ctypes.c_size_t, ctypes.c_void_p]
                 L.muon_copy_probe.restype = ctypes.c_int
                 L.muon_copy_probe.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32,
                                               ctypes.c_void_p]
@@ -809,3 +845,153 @@ def muon_attention_backward(do, q, k, v, o, lse, packing: MuonPacking, scale=Non
         _check(lib().muon_attention_backward(ctypes.byref(args), handle, ws_ptr, ws_len,
                                              ctypes.c_void_p(st.cuda_stream)))
     return outs["dq"], outs["dk"], outs["dv"]
+
+
+class MuonCheckpoint:
+    """An activation held in 8 bits (muon_checkpoint_write): `data` (uint8,
+    an opaque layout), `tokens`, `cols`."""
+
+    def __init__(self, data, tokens, cols):
+        self.data = data
+        self.tokens = int(tokens)
+        self.cols = int(cols)
+
+
+def muon_checkpoint_bytes(tokens: int, cols: int) -> int:
+    nbytes = int(lib().muon_checkpoint_bytes(int(tokens), int(cols)))
+    if nbytes == 0:
+        raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error())
+    return nbytes
+
+
+def _dtype_code(t, what):
+    import torch
+
+    if t.dtype == torch.float32:
+        return MUON_F32
+    if t.dtype == torch.bfloat16:
+        return MUON_BF16
+    raise ValueError(f"{what} must be float32 or bfloat16")
+
+
+def _matrix_view(t, what):
+    """Row stride of a 2-D GPU tensor with contiguous rows."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D GPU tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]  # one row: its stride says nothing
+
+
+def _checkpoint_items(xs, checkpoints):
+    arr = (muon_checkpoint_t * max(1, len(xs)))()
+    device = None
+    for k, (x, c) in enumerate(zip(xs, checkpoints)):
+        stride = _matrix_view(x, f"item {k}: x")
+        if x.shape != (c.tokens, c.cols):
+            raise ValueError(f"item {k}: x is {tuple(x.shape)}, the checkpoint {(c.tokens, c.cols)}")
+        device = _same_device(_same_device(device, x, f"item {k}: x"), c.data, f"item {k}: the checkpoint")
+        _checkpoint_data(c, f"item {k}")
+        arr[k] = muon_checkpoint_t(x.data_ptr(), stride, _dtype_code(x, f"item {k}: x"), 0, c.data.data_ptr(), c.tokens,
+                                   c.cols)
+    return arr, device
+
+
+def _checkpoint_data(c, what):
+    import torch
+
+    if not c.data.is_cuda or c.data.dtype != torch.uint8 or not c.data.is_contiguous():
+        raise ValueError(f"{what}: the checkpoint's data must be a contiguous uint8 GPU tensor")
+    if c.data.numel() < muon_checkpoint_bytes(c.tokens, c.cols):
+        raise ValueError(f"{what}: the checkpoint's data is too small")
+
+
+def muon_checkpoint_write(xs, checkpoints=None, stream=None) -> List[MuonCheckpoint]:
+    """Holds each (tokens, cols) activation of a list, bfloat16 or float32 with
+    contiguous rows, in 8 bits; `checkpoints` (of the same sizes) are
+    overwritten, else new ones are made."""
+    import torch
+
+    xs = list(xs)
+    if checkpoints is not None and len(checkpoints) != len(xs):
+        raise ValueError("checkpoints must hold one entry per activation")
+    if not xs:
+        return []
+    for k, x in enumerate(xs):
+        _matrix_view(x, f"item {k}: x")
+    with _on(xs[0].device, stream) as st:
+        if checkpoints is None:
+            checkpoints = [MuonCheckpoint(torch.empty(muon_checkpoint_bytes(*x.shape), dtype=torch.uint8, device=x.device),
+                                          *x.shape) for x in xs]
+        arr, _ = _checkpoint_items(xs, checkpoints)
+        _check(lib().muon_checkpoint_write(arr, len(xs), ctypes.c_void_p(st.cuda_stream)))
+    return list(checkpoints)
+
+
+def muon_checkpoint_read(checkpoints, xs=None, dtype=None, stream=None) -> List:
+    """The held values of a list of checkpoints, into `xs` (bfloat16 or
+    float32, contiguous rows) or new tensors of `dtype` (default bfloat16,
+    in which they are exact)."""
+    import torch
+
+    checkpoints = list(checkpoints)
+    if xs is not None and len(xs) != len(checkpoints):
+        raise ValueError("xs must hold one tensor per checkpoint")
+    if not checkpoints:
+        return []
+    with _on(checkpoints[0].data.device, stream) as st:
+        if xs is None:
+            xs = [torch.empty((c.tokens, c.cols), dtype=dtype or torch.bfloat16, device=c.data.device)
+                  for c in checkpoints]
+        arr, _ = _checkpoint_items(xs, checkpoints)
+        _check(lib().muon_checkpoint_read(arr, len(checkpoints), ctypes.c_void_p(st.cuda_stream)))
+    return list(xs)
+
+
+def _grad_items(matrices, accumulate):
+    import torch
+
+    arr = (muon_checkpoint_grad_t * max(1, len(matrices)))()
+    device = None
+    for k, (dy, c, G) in enumerate(matrices):
+        stride = _matrix_view(dy, f"matrix {k}: dY")
+        if dy.dtype != torch.bfloat16:
+            raise ValueError(f"matrix {k}: dY must be bfloat16")
+        if not G.is_cuda or G.dim() != 2 or not G.is_contiguous():
+            raise ValueError(f"matrix {k}: G must be a contiguous 2-D GPU tensor")
+        if dy.shape[0] != c.tokens or G.shape != (dy.shape[1], c.cols):
+            raise ValueError(f"matrix {k}: dY (tokens, outs), the checkpoint (tokens, cols) and G (outs, cols) disagree")
+        device = _same_device(_same_device(device, dy, f"matrix {k}: dY"), G, f"matrix {k}: G")
+        device = _same_device(device, c.data, f"matrix {k}: the checkpoint")
+        _checkpoint_data(c, f"matrix {k}")
+        arr[k] = muon_checkpoint_grad_t(dy.data_ptr(), stride, c.data.data_ptr(), c.tokens, c.cols, G.data_ptr(),
+                                        dy.shape[1], _dtype_code(G, f"matrix {k}: G"), int(bool(accumulate)))
+    return arr, device
+
+
+def muon_checkpoint_grad_workspace_bytes(matrices) -> int:
+    arr, _ = _grad_items(matrices, False)
+    nbytes = int(lib().muon_checkpoint_grad_workspace_bytes(arr, len(matrices)))
+    if nbytes == 0 and muon_last_error():
+        raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error())
+    return nbytes
+
+
+def muon_checkpoint_grad(matrices, accumulate=False, workspace=None, stream=None) -> None:
+    """Weight gradients of a list of (dY, checkpoint, G): G = dY^T x^ with the
+    checkpoint's held values, for dY (tokens, outs) bfloat16 with contiguous
+    rows and G (outs, cols) float32 or bfloat16, contiguous: the G of
+    muon_step.  Matrices may share a checkpoint (query, key and value
+    projections do).  accumulate adds to G instead."""
+    matrices = list(matrices)
+    if not matrices:
+        return
+    arr, device = _grad_items(matrices, accumulate)
+    need = int(lib().muon_checkpoint_grad_workspace_bytes(arr, len(matrices)))
+    if need == 0 and muon_last_error():
+        raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error())
+    with _on(device, stream) as st:
+        if workspace is None:
+            workspace = _alloc_workspace(need, device)
+        ws_ptr, ws_len = _ws_args(workspace, device)
+        _check(lib().muon_checkpoint_grad(arr, len(matrices), ws_ptr, ws_len, ctypes.c_void_p(st.cuda_stream)))

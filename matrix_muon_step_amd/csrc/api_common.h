@@ -5,6 +5,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <exception>
 #include <string>
 #include <vector>
 
@@ -32,5 +33,16 @@ struct Range {
   int64_t idx;
 };
 muon_status_t check_aliasing(std::vector<Range>& rs);
+
+// Runs the body of a C entry point, turning an exception (host memory ran out) into an error.
+template <class F>
+muon_status_t guarded(F&& f) noexcept {
+  g_last_error.clear();
+  try {
+    return f();
+  } catch (const std::exception&) {
+    return MUON_ERR_HIP;  // the message, too, would need memory
+  }
+}
 
 }  // namespace muon

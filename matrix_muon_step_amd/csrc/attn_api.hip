@@ -162,17 +162,6 @@ size_t backward_bytes(const muon_attention_grad_t* a, muon_packing_t p) {
   return align_up(static_cast<size_t>(row_stride(p)) * a->heads * 2 * sizeof(float));
 }
 
-// Runs f, turning an exception (host memory ran out) into an error.
-template <class F>
-muon_status_t guarded(F&& f) noexcept {
-  g_last_error.clear();
-  try {
-    return f();
-  } catch (const std::exception&) {
-    return MUON_ERR_INVALID_ARG;
-  }
-}
-
 }  // namespace
 
 extern "C" {
