@@ -49,24 +49,18 @@ constexpr float kSlackLog2 = 8.f;
 
 template <int DP>
 struct Geo {
-  static constexpr int NC = DP / 8;           // 16-byte chunks of a row
-  static constexpr int PITCH = DP * 2;        // bytes of a row
   static constexpr int KS = DP / 16;          // 16-deep steps over the head dimension
   static constexpr int DB = DP / 32;          // 32-wide blocks of the head dimension
-  static constexpr int TILEB = kAttnStep * PITCH;  // bytes of a streamed tile
-  static constexpr int NI = kAttnStep * NC / 256;  // 16-byte loads per lane and tile (4 waves)
+  static constexpr int SUBB = kAttnStep * 64; // bytes of one 32-wide block of a streamed tile
+  static constexpr int TILEB = DB * SUBB;     // bytes of a streamed tile
 };
 
-// Position of chunk c in row r of an LDS tile: c ^ swz.  Both readers are
-// free of bank conflicts with it: 16 rows at one chunk (ordinary 16-byte
-// fragment reads) and 4 rows at 4 chunks (transposing reads) each touch all
-// 64 banks once.  Repeats every 16 rows; only its upper bits depend on the
-// 64-byte group, so a fragment's address moves to another k-step or 32-wide
-// block by an exclusive or.
-template <int DP>
-__device__ __forceinline__ int tile_swz(int r) {
-  return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-}
+// A streamed tile of 64 rows lies in LDS as its 32-wide blocks one after
+// another, each 64 rows of 64 bytes, with the row's four 16-byte chunks
+// exclusive-or'ed by swz (muon_internal.h).  Both readers are free of bank
+// conflicts with it (ordinary 16-byte reads of 32 rows; transposing reads of
+// four whole rows), and since the pattern repeats every 16 rows, every
+// fragment is one of four lane addresses plus a constant.
 
 // Direct-to-LDS load of 16 (WORD: 4) bytes a lane, lane i to dst + 16 i (4 i),
 // from base + off, zero from byte `bytes` on.  base, bytes and dst are the
@@ -87,41 +81,33 @@ __device__ __forceinline__ void load_lds(const unsigned char* base, uint32_t byt
 #endif
 }
 
-constexpr uint32_t kOutside = 0xC0000000u;  // an offset past every descriptor (their sizes stay below 2^31)
+constexpr uint32_t kOutside = 0xC0000000u;  // an offset past every buffer's size (those stay below 2^31)
 
-// Offsets of a lane's 16-byte loads of a 64-row tile, relative to the tile's
-// first row; chunks beyond the head dimension read as zero.
-template <int DP>
-struct LoadOff {
-  uint32_t off[Geo<DP>::NI];
+// A lane's part of the loads of a tensor's tiles: 16 rows x 64 bytes per
+// load, row lane / 4, the chunk that the swizzle puts at place lane % 4.
+struct LoadLane {
+  uint32_t off;   // bytes from the load's first row and block
+  int elem;       // first element of the chunk within the block
 };
-template <int DP>
-__device__ __forceinline__ LoadOff<DP> load_offsets(int wave, int lane, int64_t ts, int head_dim) {
-  using G = Geo<DP>;
-  LoadOff<DP> r;
+__device__ __forceinline__ LoadLane load_lane(int lane, int64_t ts) {
+  const int row = lane >> 2, c = swz(row, lane & 3);
+  return {static_cast<uint32_t>(row) * static_cast<uint32_t>(ts * 2) + c * 16, c * 8};
+}
+
+// Starts the loads of a 64-row tile into LDS by NW waves.  base: the tile's
+// first row; rows: rows the sequence has from there on.  Rows past them and
+// elements past the head dimension are zero in LDS.
+template <int DP, int NW>
+__device__ __forceinline__ void load_tile(const unsigned char* base, int rows, int64_t ts, int head_dim,
+                                          const LoadLane& l, LAS unsigned char* __restrict__ dst, int wave) {
 #pragma unroll
-  for (int i = 0; i < G::NI; ++i) {
-    const int p = (wave + i * 4) * 64 + lane;
-    const int row = p / G::NC;
-    const int c = (p % G::NC) ^ tile_swz<DP>(row);
-    r.off[i] = c * 8 < head_dim ? static_cast<uint32_t>(row) * static_cast<uint32_t>(ts * 2) + c * 16 : kOutside;
+  for (int i = 0; i < DP / 8 / NW; ++i) {
+    const int q = wave + i * NW, db = q >> 2, r0 = 16 * (q & 3);
+    const int n = min(rows - r0, 16);
+    const uint32_t bytes = n <= 0 ? 0u : static_cast<uint32_t>((n - 1) * (ts * 2)) + 2 * (head_dim - 32 * db);
+    load_lds<false>(base + (r0 * ts + 32 * db) * 2, 32 * db < head_dim ? bytes : 0u,
+                    l.elem < head_dim - 32 * db ? l.off : kOutside, dst + q * 1024);
   }
-  return r;
-}
-
-// Bytes that rows first .. of a sequence of `len` rows hold behind the
-// address of row `first` (rows beyond the tile are never addressed).
-__device__ __forceinline__ uint32_t rows_bytes(int len, int first, int64_t ts, int head_dim, int most) {
-  const int rows = min(len - first, most);
-  return rows <= 0 ? 0u : static_cast<uint32_t>((rows - 1) * (ts * 2) + head_dim * 2);
-}
-
-// Starts the loads of one 64-row tile into LDS (direct, 16 bytes a lane).
-template <int DP>
-__device__ __forceinline__ void load_tile(const unsigned char* base, uint32_t bytes, const LoadOff<DP>& lo,
-                                          LAS unsigned char* __restrict__ dst, int wave) {
-#pragma unroll
-  for (int i = 0; i < Geo<DP>::NI; ++i) load_lds<false>(base, bytes, lo.off[i], dst + (wave + i * 4) * 1024);
 }
 
 __device__ __forceinline__ bf16x8_t join4(bf16x4_t lo, bf16x4_t hi) {
@@ -129,25 +115,21 @@ __device__ __forceinline__ bf16x8_t join4(bf16x4_t lo, bf16x4_t hi) {
 }
 
 // Lane addresses of the two fragment readers, in bytes within a tile.
-//   row: 16-byte read of row (lane & 31), chunk 2 s + (lane >> 5): row ^ (32 s)
-//   tr[e]: transposing read of rows 8e + 4h + 0..3, 32-wide block db:
-//          tr[e] ^ (64 db); 16 rows further: + 16 PITCH
-template <int DP>
+//   row[e]: 16-byte read of row (lane & 31), chunk 2 e + (lane >> 5) of a block
+//   tr[e]:  transposing read of rows 8 e + 4 (lane >> 5) + 0..3 of a block
 struct FragOff {
-  int row;
+  int row[2];
   int tr[2];
 };
-template <int DP>
-__device__ __forceinline__ FragOff<DP> frag_offsets(int lane) {
-  using G = Geo<DP>;
-  FragOff<DP> f;
+__device__ __forceinline__ FragOff frag_offsets(int lane) {
+  FragOff f;
   const int r = lane & 31, h = lane >> 5;
-  f.row = r * G::PITCH + ((h ^ tile_swz<DP>(r)) << 4);
-  const int cl = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  f.row[0] = r * 64 + swz(r, h) * 16;
+  f.row[1] = r * 64 + swz(r, 2 + h) * 16;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int tr = 8 * e + 4 * h + ((lane & 15) >> 2);
-    f.tr[e] = tr * G::PITCH + ((cl ^ tile_swz<DP>(tr)) << 4) + (lane & 1) * 8;
+    f.tr[e] = tr * 64 + swz(tr, 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) * 16 + (lane & 1) * 8;
   }
   return f;
 }
@@ -155,19 +137,17 @@ __device__ __forceinline__ FragOff<DP> frag_offsets(int lane) {
 // Left operand of a product over the head dimension: rows 32 b + 0..31 of a
 // tile, k-step s.
 template <int DP>
-__device__ __forceinline__ bf16x8_t row_frag(const LAS unsigned char* __restrict__ t, const FragOff<DP>& f, int b,
-                                             int s) {
-  return *(const LAS bf16x8_t*)(t + (f.row ^ (s * 32)) + b * 32 * Geo<DP>::PITCH);
+__device__ __forceinline__ bf16x8_t row_frag(const LAS unsigned char* __restrict__ t, const FragOff& f, int b, int s) {
+  return *(const LAS bf16x8_t*)(t + f.row[s & 1] + (s >> 1) * Geo<DP>::SUBB + b * 2048);
 }
 // Left operand of a product over rows: columns 32 db + 0..31 of a tile,
 // rows 16 t16 + 0..15 in the order of the results' registers.
 template <int DP>
-__device__ __forceinline__ bf16x8_t col_frag(const LAS unsigned char* __restrict__ t, const FragOff<DP>& f, int db,
+__device__ __forceinline__ bf16x8_t col_frag(const LAS unsigned char* __restrict__ t, const FragOff& f, int db,
                                              int t16) {
-  const LAS unsigned char* p0 = t + (f.tr[0] ^ (db * 64)) + t16 * 16 * Geo<DP>::PITCH;
-  const LAS unsigned char* p1 = t + (f.tr[1] ^ (db * 64)) + t16 * 16 * Geo<DP>::PITCH;
-  return join4(__builtin_amdgcn_ds_read_tr16_b64_v4bf16((LAS bf16x4_t*)p0),
-               __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LAS bf16x4_t*)p1));
+  const LAS unsigned char* p = t + db * Geo<DP>::SUBB + t16 * 1024;
+  return join4(__builtin_amdgcn_ds_read_tr16_b64_v4bf16((LAS bf16x4_t*)(p + f.tr[0])),
+               __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LAS bf16x4_t*)(p + f.tr[1])));
 }
 
 // Registers 8 s .. 8 s + 7 of a float32 result as a bf16 operand.
@@ -271,16 +251,14 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(const AttnArgs a) {
 
   const unsigned char* kbase = a.k.p + (t.row0 * a.k.ts + kv * a.k.hs) * 2;
   const unsigned char* vbase = a.v.p + (t.row0 * a.v.ts + kv * a.v.hs) * 2;
-  const LoadOff<DP> ko = load_offsets<DP>(wave, lane, a.k.ts, a.head_dim);
-  const LoadOff<DP> vo = load_offsets<DP>(wave, lane, a.v.ts, a.head_dim);
-  const FragOff<DP> fo = frag_offsets<DP>(lane);
+  const LoadLane ko = load_lane(lane, a.k.ts);
+  const LoadLane vo = load_lane(lane, a.v.ts);
+  const FragOff fo = frag_offsets(lane);
   auto issue = [&](int kt) {
     LAS unsigned char* dst = lds + (kt & 1) * 2 * G::TILEB;
     const int k0 = kt * kAttnStep;
-    load_tile<DP>(kbase + static_cast<int64_t>(k0) * a.k.ts * 2, rows_bytes(t.len, k0, a.k.ts, a.head_dim, kAttnStep), ko, dst,
-                  wave);
-    load_tile<DP>(vbase + static_cast<int64_t>(k0) * a.v.ts * 2, rows_bytes(t.len, k0, a.v.ts, a.head_dim, kAttnStep), vo,
-                  dst + G::TILEB, wave);
+    load_tile<DP, 4>(kbase + k0 * a.k.ts * 2, t.len - k0, a.k.ts, a.head_dim, ko, dst, wave);
+    load_tile<DP, 4>(vbase + k0 * a.v.ts * 2, t.len - k0, a.v.ts, a.head_dim, vo, dst + G::TILEB, wave);
   };
   issue(0);
   bf16x8_t qf[G::KS];
@@ -364,7 +342,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(const AttnArgs a) {
 // value tiles stream past.  Also forms delta and leaves it, with lse in
 // base 2, for the dK/dV kernel that follows.
 template <int DP>
-__global__ __launch_bounds__(256, 1) void attention_dq_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void attention_dq_kernel(const AttnArgs a) {
   using G = Geo<DP>;
   __shared__ __align__(1024) unsigned char smem[4 * G::TILEB];
   LAS unsigned char* lds = (LAS unsigned char*)smem;
@@ -383,16 +361,14 @@ __global__ __launch_bounds__(256, 1) void attention_dq_kernel(const AttnArgs a) 
 
   const unsigned char* kbase = a.k.p + (t.row0 * a.k.ts + kv * a.k.hs) * 2;
   const unsigned char* vbase = a.v.p + (t.row0 * a.v.ts + kv * a.v.hs) * 2;
-  const LoadOff<DP> ko = load_offsets<DP>(wave, lane, a.k.ts, a.head_dim);
-  const LoadOff<DP> vo = load_offsets<DP>(wave, lane, a.v.ts, a.head_dim);
-  const FragOff<DP> fo = frag_offsets<DP>(lane);
+  const LoadLane ko = load_lane(lane, a.k.ts);
+  const LoadLane vo = load_lane(lane, a.v.ts);
+  const FragOff fo = frag_offsets(lane);
   auto issue = [&](int kt) {
     LAS unsigned char* dst = lds + (kt & 1) * 2 * G::TILEB;
     const int k0 = kt * kAttnStep;
-    load_tile<DP>(kbase + static_cast<int64_t>(k0) * a.k.ts * 2, rows_bytes(t.len, k0, a.k.ts, a.head_dim, kAttnStep), ko, dst,
-                  wave);
-    load_tile<DP>(vbase + static_cast<int64_t>(k0) * a.v.ts * 2, rows_bytes(t.len, k0, a.v.ts, a.head_dim, kAttnStep), vo,
-                  dst + G::TILEB, wave);
+    load_tile<DP, 4>(kbase + k0 * a.k.ts * 2, t.len - k0, a.k.ts, a.head_dim, ko, dst, wave);
+    load_tile<DP, 4>(vbase + k0 * a.v.ts * 2, t.len - k0, a.v.ts, a.head_dim, vo, dst + G::TILEB, wave);
   };
   issue(0);
   const int64_t row0 = static_cast<int64_t>(t.row0) + wq0;
@@ -451,15 +427,28 @@ __global__ __launch_bounds__(256, 1) void attention_dq_kernel(const AttnArgs a) 
 }
 
 // -------------------------------------------------------- backward: dK, dV
-// One work-group: 128 key rows of one key head, 4 waves of 32 keys; the
-// query and upstream-gradient tiles of every query head of the group stream
-// past, so that the sums over rows and heads stay in registers, in a fixed
-// order.
+// One work-group: 128 key rows of one key head; the query and
+// upstream-gradient tiles of every query head of the group stream past, so
+// that the sums over rows and heads stay in registers, in a fixed order.
+// 8 waves, two per SIMD: wave w holds keys 32 (w & 3) .. + 31 and takes rows
+// 32 (w >> 2) .. + 31 of each 64-row tile; the two partial sums of a key are
+// joined through LDS at the end.
 template <int DP>
-__global__ __launch_bounds__(256, 1) void attention_dkv_kernel(const AttnArgs a) {
+struct DkvLds {
+  static constexpr int ROWS = 2 * Geo<DP>::TILEB;             // q and dO tiles, then lse and delta
+  static constexpr int STAGE = ROWS + 2 * kAttnStep * 4;
+  static constexpr int JOIN = 4 * 64 * Geo<DP>::DB * 16 * 4;  // one accumulator of 4 waves
+  static constexpr int BYTES = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
+};
+
+// Four consecutive per-row values of a tile.
+__device__ __forceinline__ f32x4_t row_values(const LAS unsigned char* __restrict__ p) { return *(const LAS f32x4_t*)p; }
+
+template <int DP>
+__global__ __launch_bounds__(512, 2) void attention_dkv_kernel(const AttnArgs a) {
   using G = Geo<DP>;
-  constexpr int STAGE = 2 * G::TILEB + 2 * kAttnStep * 4;
-  __shared__ __align__(1024) unsigned char smem[2 * STAGE];
+  using L = DkvLds<DP>;
+  __shared__ __align__(1024) unsigned char smem[L::BYTES];
   LAS unsigned char* lds = (LAS unsigned char*)smem;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -468,26 +457,25 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(const AttnArgs a)
   const int group = a.heads / a.kv_heads;
   const int nq = (t.len - t.first + kAttnStep - 1) / kAttnStep;  // query tiles from the diagonal on
   const int total = nq * group;
-  const int wk0 = t.first + 32 * wave;
+  const int wk0 = t.first + 32 * (wave & 3), b = wave >> 2;
   const int key = wk0 + (lane & 31);
   const float c = a.scale * kLog2e;
 
-  const LoadOff<DP> qo = load_offsets<DP>(wave, lane, a.q.ts, a.head_dim);
-  const LoadOff<DP> go = load_offsets<DP>(wave, lane, a.d_o.ts, a.head_dim);
-  const FragOff<DP> fo = frag_offsets<DP>(lane);
+  const LoadLane qo = load_lane(lane, a.q.ts);
+  const LoadLane go = load_lane(lane, a.d_o.ts);
+  const FragOff fo = frag_offsets(lane);
   auto issue = [&](int it) {
-    LAS unsigned char* dst = lds + (it & 1) * STAGE;
+    LAS unsigned char* dst = lds + (it & 1) * L::STAGE;
     const int head = kv * group + it / nq;
     const int q0 = t.first + (it % nq) * kAttnStep;
     const int64_t row = static_cast<int64_t>(t.row0) + q0;
-    load_tile<DP>(a.q.p + (row * a.q.ts + head * a.q.hs) * 2, rows_bytes(t.len, q0, a.q.ts, a.head_dim, kAttnStep), qo, dst,
-                  wave);
-    load_tile<DP>(a.d_o.p + (row * a.d_o.ts + head * a.d_o.hs) * 2,
-                  rows_bytes(t.len, q0, a.d_o.ts, a.head_dim, kAttnStep), go, dst + G::TILEB, wave);
+    load_tile<DP, 8>(a.q.p + (row * a.q.ts + head * a.q.hs) * 2, t.len - q0, a.q.ts, a.head_dim, qo, dst, wave);
+    load_tile<DP, 8>(a.d_o.p + (row * a.d_o.ts + head * a.d_o.hs) * 2, t.len - q0, a.d_o.ts, a.head_dim, go,
+                     dst + G::TILEB, wave);
     if (wave < 2) {
       const float* src = (wave == 0 ? a.row_lse2 : a.row_delta) + head * a.row_stride + row;
       load_lds<true>(reinterpret_cast<const unsigned char*>(src), 4u * min(t.len - q0, kAttnStep), lane * 4,
-                  dst + 2 * G::TILEB + wave * kAttnStep * 4);
+                     dst + L::ROWS + wave * kAttnStep * 4);
     }
   };
   issue(0);
@@ -502,50 +490,68 @@ __global__ __launch_bounds__(256, 1) void attention_dkv_kernel(const AttnArgs a)
   for (int it = 0; it < total; ++it) {
     next_tile();
     if (it + 1 < total) issue(it + 1);
-    if (wk0 >= t.len) continue;
-    const int q0 = t.first + (it % nq) * kAttnStep;
-    const LAS unsigned char* qt = lds + (it & 1) * STAGE;
+    const int qs = t.first + (it % nq) * kAttnStep + 32 * b;
+    if (qs + 31 < wk0 || qs >= t.len || wk0 >= t.len) continue;  // no query of the block sees a key of the wave
+    const LAS unsigned char* qt = lds + (it & 1) * L::STAGE;
     const LAS unsigned char* gt = qt + G::TILEB;
-    const LAS float* rows_lse = (const LAS float*)(qt + 2 * G::TILEB);
-    const LAS float* rows_delta = rows_lse + kAttnStep;
+    f32x16_t s = (f32x16_t)(0.f), dp = (f32x16_t)(0.f);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int qs = q0 + 32 * b;
-      if (qs + 31 < wk0 || qs >= t.len) continue;  // no query of the block sees a key of the wave
-      f32x16_t s = (f32x16_t)(0.f), dp = (f32x16_t)(0.f);
+    for (int st = 0; st < G::KS; ++st) s = mfma(row_frag<DP>(qt, fo, b, st), kf[st], s);
 #pragma unroll
-      for (int st = 0; st < G::KS; ++st) s = mfma(row_frag<DP>(qt, fo, b, st), kf[st], s);
+    for (int st = 0; st < G::KS; ++st) dp = mfma(row_frag<DP>(gt, fo, b, st), vf[st], dp);
+    const bool edge = qs < wk0 + 31 || qs + 31 >= t.len;
 #pragma unroll
-      for (int st = 0; st < G::KS; ++st) dp = mfma(row_frag<DP>(gt, fo, b, st), vf[st], dp);
-      const bool edge = qs < wk0 + 31 || qs + 31 >= t.len;
+    for (int g = 0; g < 4; ++g) {
+      const f32x4_t lse2 = row_values(qt + L::ROWS + (32 * b + 8 * g + 4 * h) * 4);
+      const f32x4_t delta = row_values(qt + L::ROWS + (kAttnStep + 32 * b + 8 * g + 4 * h) * 4);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4_t lse2 = *(const LAS f32x4_t*)(rows_lse + 32 * b + 8 * g + 4 * h);
-        const f32x4_t delta = *(const LAS f32x4_t*)(rows_delta + 32 * b + 8 * g + 4 * h);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 4 * g + i, q = qs + 8 * g + 4 * h + i;
-          float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2[i]));
-          float ds = p * (dp[r] - delta[i]);
-          if (edge && (key > q || q >= t.len)) p = ds = 0.f;
-          s[r] = p;
-          dp[r] = ds;
-        }
-      }
-#pragma unroll
-      for (int s16 = 0; s16 < 2; ++s16) {
-        const bf16x8_t p = to_operand(s, s16), ds = to_operand(dp, s16);
-#pragma unroll
-        for (int db = 0; db < G::DB; ++db) dv[db] = mfma(col_frag<DP>(gt, fo, db, 2 * b + s16), p, dv[db]);
-#pragma unroll
-        for (int db = 0; db < G::DB; ++db) dk[db] = mfma(col_frag<DP>(qt, fo, db, 2 * b + s16), ds, dk[db]);
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * g + i, q = qs + 8 * g + 4 * h + i;
+        float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2[i]));
+        float ds = p * (dp[r] - delta[i]);
+        if (edge && (key > q || q >= t.len)) p = ds = 0.f;
+        s[r] = p;
+        dp[r] = ds;
       }
     }
+#pragma unroll
+    for (int s16 = 0; s16 < 2; ++s16) {
+      const bf16x8_t p = to_operand(s, s16), ds = to_operand(dp, s16);
+#pragma unroll
+      for (int db = 0; db < G::DB; ++db) dv[db] = mfma(col_frag<DP>(gt, fo, db, 2 * b + s16), p, dv[db]);
+#pragma unroll
+      for (int db = 0; db < G::DB; ++db) dk[db] = mfma(col_frag<DP>(qt, fo, db, 2 * b + s16), ds, dk[db]);
+    }
   }
+  // Waves 4..7 hand their sums to waves 0..3, dk first, then dv.
   const bool live = key < t.len;
   const int64_t row = static_cast<int64_t>(t.row0) + key;
-  store_rows<DP>(a.dk, row, kv, a.head_dim, live, lane, dk, a.scale);
-  store_rows<DP>(a.dv, row, kv, a.head_dim, live, lane, dv, 1.f);
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    f32x16_t(&acc)[G::DB] = part == 0 ? dk : dv;
+    LAS float* at = (LAS float*)lds + ((wave & 3) * 64 + lane) * 4;
+    next_tile();
+    if (b == 1) {
+#pragma unroll
+      for (int db = 0; db < G::DB; ++db)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *(LAS f32x4_t*)(at + (db * 4 + g) * 1024) =
+              (f32x4_t){acc[db][4 * g], acc[db][4 * g + 1], acc[db][4 * g + 2], acc[db][4 * g + 3]};
+    }
+    next_tile();
+    if (b == 0) {
+#pragma unroll
+      for (int db = 0; db < G::DB; ++db)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4_t o = *(const LAS f32x4_t*)(at + (db * 4 + g) * 1024);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[db][4 * g + i] += o[i];
+        }
+      store_rows<DP>(part == 0 ? a.dk : a.dv, row, kv, a.head_dim, live, lane, acc, part == 0 ? a.scale : 1.f);
+    }
+  }
 }
 
 }  // namespace
@@ -561,10 +567,10 @@ hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s) {
   const dim3 gq(static_cast<uint32_t>(a.n_tiles) * a.heads), gk(static_cast<uint32_t>(a.n_tiles) * a.kv_heads);
   if (a.head_dim <= 64) {
     hipLaunchKernelGGL(attention_dq_kernel<64>, gq, dim3(256), 0, s, a);
-    hipLaunchKernelGGL(attention_dkv_kernel<64>, gk, dim3(256), 0, s, a);
+    hipLaunchKernelGGL(attention_dkv_kernel<64>, gk, dim3(512), 0, s, a);
   } else {
     hipLaunchKernelGGL(attention_dq_kernel<128>, gq, dim3(256), 0, s, a);
-    hipLaunchKernelGGL(attention_dkv_kernel<128>, gk, dim3(256), 0, s, a);
+    hipLaunchKernelGGL(attention_dkv_kernel<128>, gk, dim3(512), 0, s, a);
   }
   return hipGetLastError();
 }
