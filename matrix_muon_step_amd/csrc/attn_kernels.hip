@@ -62,53 +62,62 @@ struct Geo {
 // four whole rows), and since the pattern repeats every 16 rows, every
 // fragment is one of four lane addresses plus a constant.
 
-// Direct-to-LDS load of 16 (WORD: 4) bytes a lane, lane i to dst + 16 i (4 i),
-// from base + off, zero from byte `bytes` on.  base, bytes and dst are the
-// same in every lane.
-template <bool WORD>
+constexpr uint32_t kOutside = 0xC0000000u;  // an offset past every buffer's size (those stay below 2^31)
+
+// Direct-to-LDS loads, 16 (WORD: 4) bytes a lane, lane i to dst + 16 i (4 i),
+// from base + off + IMM, zero from byte `bytes` on.  base, bytes and dst are
+// the same in every lane.  The instruction adds IMM to both of its addresses.
+template <bool WORD, int IMM>
 __device__ __forceinline__ void load_lds(const unsigned char* base, uint32_t bytes, uint32_t off,
-                                         LAS unsigned char* dst) {
+                                         LAS unsigned char* __restrict__ dst) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  const uintptr_t a = reinterpret_cast<uintptr_t>(base);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
-  void* p = reinterpret_cast<void*>((static_cast<uintptr_t>(hi) << 32) | lo);
   // untyped, no stride: offsets are compared with the size in bytes
-  const __amdgpu_buffer_rsrc_t r =
-      __builtin_amdgcn_make_buffer_rsrc(p, 0, __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
-  if (WORD) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LAS void*)dst, 4, off, 0, 0, 0);
-  else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LAS void*)dst, 16, off, 0, 0, 0);
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<unsigned char*>(base), 0, bytes, 0x00020000);
+  if (WORD) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LAS void*)(dst - IMM), 4, off, 0, IMM, 0);
+  else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LAS void*)(dst - IMM), 16, off, 0, IMM, 0);
 #endif
 }
 
-constexpr uint32_t kOutside = 0xC0000000u;  // an offset past every buffer's size (those stay below 2^31)
+// A wave's share of the loads of a tensor's 64-row tiles: 16 rows (16 (wave &
+// 3) on) x 64 bytes per load, lane i row i / 4 and the chunk that the swizzle
+// puts at place i % 4.  NW waves: loads for blocks (wave >> 2) + NW / 4 * i.
+// EXACT: the head dimension is DP, else elements past it read as zero.  So do
+// rows past the sequence.
+template <int DP, bool EXACT, int NW>
+struct TileLoad {
+  static constexpr int N = DP / 8 / NW;  // loads per tile
+  const unsigned char* p;                // the wave's first row of the next tile
+  uint32_t off;
+  int ts2, tail, dim, chunk;             // bytes of a token; valid bytes of a row from p on; EXACT only: -
 
-// A lane's part of the loads of a tensor's tiles: 16 rows x 64 bytes per
-// load, row lane / 4, the chunk that the swizzle puts at place lane % 4.
-struct LoadLane {
-  uint32_t off;   // bytes from the load's first row and block
-  int elem;       // first element of the chunk within the block
-};
-__device__ __forceinline__ LoadLane load_lane(int lane, int64_t ts) {
-  const int row = lane >> 2, c = swz(row, lane & 3);
-  return {static_cast<uint32_t>(row) * static_cast<uint32_t>(ts * 2) + c * 16, c * 8};
-}
-
-// Starts the loads of a 64-row tile into LDS by NW waves.  base: the tile's
-// first row; rows: rows the sequence has from there on.  Rows past them and
-// elements past the head dimension are zero in LDS.
-template <int DP, int NW>
-__device__ __forceinline__ void load_tile(const unsigned char* base, int rows, int64_t ts, int head_dim,
-                                          const LoadLane& l, LAS unsigned char* __restrict__ dst, int wave) {
-#pragma unroll
-  for (int i = 0; i < DP / 8 / NW; ++i) {
-    const int q = wave + i * NW, db = q >> 2, r0 = 16 * (q & 3);
-    const int n = min(rows - r0, 16);
-    const uint32_t bytes = n <= 0 ? 0u : static_cast<uint32_t>((n - 1) * (ts * 2)) + 2 * (head_dim - 32 * db);
-    load_lds<false>(base + (r0 * ts + 32 * db) * 2, 32 * db < head_dim ? bytes : 0u,
-                    l.elem < head_dim - 32 * db ? l.off : kOutside, dst + q * 1024);
+  __device__ __forceinline__ TileLoad(const HeadsView& v, int64_t row, int head, int head_dim, int wave, int lane) {
+    const int r = lane >> 2, c = swz(r, lane & 3), db0 = wave >> 2;
+    ts2 = static_cast<int>(v.ts * 2);
+    p = v.p + ((row + 16 * (wave & 3)) * v.ts + head * v.hs) * 2 + 64 * db0;
+    off = static_cast<uint32_t>(r) * static_cast<uint32_t>(ts2) + c * 16;
+    tail = 2 * (head_dim - 32 * db0);
+    dim = head_dim - 32 * db0;
+    chunk = c * 8;
   }
-}
+  __device__ __forceinline__ void move(int64_t bytes) { p += bytes; }
+  template <int I>
+  __device__ __forceinline__ void one(uint32_t bytes, LAS unsigned char* __restrict__ dst, int wave) const {
+    uint32_t at = off;
+    if (!EXACT && chunk >= dim - 8 * NW * I) at = kOutside;
+    load_lds<false, 16 * NW * I>(p, bytes, at, dst + (wave + I * NW) * 1024);
+  }
+  // rows: what the sequence has from the tile's first row on.
+  __device__ __forceinline__ void load(int rows, LAS unsigned char* __restrict__ dst, int wave) const {
+    const int n = min(rows - 16 * (wave & 3), 16);
+    const uint32_t bytes = n <= 0 || (!EXACT && tail <= 0) ? 0u : static_cast<uint32_t>((n - 1) * ts2 + tail);
+    one<0>(bytes, dst, wave);
+    if constexpr (N > 1) one<1>(bytes, dst, wave);
+    if constexpr (N > 2) {
+      one<2>(bytes, dst, wave);
+      one<3>(bytes, dst, wave);
+    }
+  }
+};
 
 __device__ __forceinline__ bf16x8_t join4(bf16x4_t lo, bf16x4_t hi) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -232,7 +241,7 @@ __device__ __forceinline__ void atomic_max_float(float* p, float x) {
 // ------------------------------------------------------------------ forward
 // One work-group: 128 query rows of one head, 4 waves of 32 rows; key and
 // value tiles of 64 rows stream through a double buffer in LDS.
-template <int DP>
+template <int DP, bool EXACT>
 __global__ __launch_bounds__(256, 2) void attention_kernel(const AttnArgs a) {
   using G = Geo<DP>;
   __shared__ __align__(1024) unsigned char smem[4 * G::TILEB];
@@ -249,18 +258,18 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(const AttnArgs a) {
   const float c = a.scale * kLog2e;
   const float slack = kSlackLog2 / c;
 
-  const unsigned char* kbase = a.k.p + (t.row0 * a.k.ts + kv * a.k.hs) * 2;
-  const unsigned char* vbase = a.v.p + (t.row0 * a.v.ts + kv * a.v.hs) * 2;
-  const LoadLane ko = load_lane(lane, a.k.ts);
-  const LoadLane vo = load_lane(lane, a.v.ts);
+  TileLoad<DP, EXACT, 4> kl(a.k, t.row0, kv, a.head_dim, wave, lane), vl(a.v, t.row0, kv, a.head_dim, wave, lane);
   const FragOff fo = frag_offsets(lane);
-  auto issue = [&](int kt) {
-    LAS unsigned char* dst = lds + (kt & 1) * 2 * G::TILEB;
-    const int k0 = kt * kAttnStep;
-    load_tile<DP, 4>(kbase + k0 * a.k.ts * 2, t.len - k0, a.k.ts, a.head_dim, ko, dst, wave);
-    load_tile<DP, 4>(vbase + k0 * a.v.ts * 2, t.len - k0, a.v.ts, a.head_dim, vo, dst + G::TILEB, wave);
+  int fill = 0, fill_row = 0;  // the buffer (byte offset) and first key of the next tile to load
+  auto issue = [&]() {
+    kl.load(t.len - fill_row, lds + fill, wave);
+    vl.load(t.len - fill_row, lds + fill + G::TILEB, wave);
+    kl.move(static_cast<int64_t>(kl.ts2) * kAttnStep);
+    vl.move(static_cast<int64_t>(vl.ts2) * kAttnStep);
+    fill_row += kAttnStep;
+    fill ^= 2 * G::TILEB;
   };
-  issue(0);
+  issue();
   bf16x8_t qf[G::KS];
   own_rows<DP>(a.q.p + ((static_cast<int64_t>(t.row0) + wq0) * a.q.ts + head * a.q.hs) * 2, a.q.ts, a.head_dim, t.len - wq0,
                lane, qf);
@@ -270,11 +279,11 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(const AttnArgs a) {
   for (int db = 0; db < G::DB; ++db) o[db] = (f32x16_t)(0.f);
   float m_top = -kInf, m_ref = -kInf, l = 0.f;  // l: this lane's half of the keys
   for (int kt = 0; kt < nk; ++kt) {
-    const int k0 = kt * kAttnStep;
+    const int k0 = kt * kAttnStep, cur = fill ^ (2 * G::TILEB);
     next_tile();
-    if (kt + 1 < nk) issue(kt + 1);
+    if (kt + 1 < nk) issue();
     if (k0 > wq0 + 31) continue;  // every key lies behind the wave's rows
-    const LAS unsigned char* kt_lds = lds + (kt & 1) * 2 * G::TILEB;
+    const LAS unsigned char* kt_lds = lds + cur;
     const LAS unsigned char* vt_lds = kt_lds + G::TILEB;
     f32x16_t s[2];
 #pragma unroll
@@ -341,7 +350,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(const AttnArgs a) {
 // One work-group: 128 query rows of one head, 4 waves of 32 rows; key and
 // value tiles stream past.  Also forms delta and leaves it, with lse in
 // base 2, for the dK/dV kernel that follows.
-template <int DP>
+template <int DP, bool EXACT>
 __global__ __launch_bounds__(256, 2) void attention_dq_kernel(const AttnArgs a) {
   using G = Geo<DP>;
   __shared__ __align__(1024) unsigned char smem[4 * G::TILEB];
@@ -359,18 +368,18 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(const AttnArgs a) 
   const int64_t row = static_cast<int64_t>(t.row0) + q;
   const float c = a.scale * kLog2e;
 
-  const unsigned char* kbase = a.k.p + (t.row0 * a.k.ts + kv * a.k.hs) * 2;
-  const unsigned char* vbase = a.v.p + (t.row0 * a.v.ts + kv * a.v.hs) * 2;
-  const LoadLane ko = load_lane(lane, a.k.ts);
-  const LoadLane vo = load_lane(lane, a.v.ts);
+  TileLoad<DP, EXACT, 4> kl(a.k, t.row0, kv, a.head_dim, wave, lane), vl(a.v, t.row0, kv, a.head_dim, wave, lane);
   const FragOff fo = frag_offsets(lane);
-  auto issue = [&](int kt) {
-    LAS unsigned char* dst = lds + (kt & 1) * 2 * G::TILEB;
-    const int k0 = kt * kAttnStep;
-    load_tile<DP, 4>(kbase + k0 * a.k.ts * 2, t.len - k0, a.k.ts, a.head_dim, ko, dst, wave);
-    load_tile<DP, 4>(vbase + k0 * a.v.ts * 2, t.len - k0, a.v.ts, a.head_dim, vo, dst + G::TILEB, wave);
+  int fill = 0, fill_row = 0;  // the buffer (byte offset) and first key of the next tile to load
+  auto issue = [&]() {
+    kl.load(t.len - fill_row, lds + fill, wave);
+    vl.load(t.len - fill_row, lds + fill + G::TILEB, wave);
+    kl.move(static_cast<int64_t>(kl.ts2) * kAttnStep);
+    vl.move(static_cast<int64_t>(vl.ts2) * kAttnStep);
+    fill_row += kAttnStep;
+    fill ^= 2 * G::TILEB;
   };
-  issue(0);
+  issue();
   const int64_t row0 = static_cast<int64_t>(t.row0) + wq0;
   bf16x8_t qf[G::KS], gf[G::KS];
   own_rows<DP>(a.q.p + (row0 * a.q.ts + head * a.q.hs) * 2, a.q.ts, a.head_dim, t.len - wq0, lane, qf);
@@ -395,11 +404,11 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(const AttnArgs a) 
 #pragma unroll
   for (int db = 0; db < G::DB; ++db) dq[db] = (f32x16_t)(0.f);
   for (int kt = 0; kt < nk; ++kt) {
-    const int k0 = kt * kAttnStep;
+    const int k0 = kt * kAttnStep, cur = fill ^ (2 * G::TILEB);
     next_tile();
-    if (kt + 1 < nk) issue(kt + 1);
+    if (kt + 1 < nk) issue();
     if (k0 > wq0 + 31) continue;
-    const LAS unsigned char* kt_lds = lds + (kt & 1) * 2 * G::TILEB;
+    const LAS unsigned char* kt_lds = lds + cur;
     const LAS unsigned char* vt_lds = kt_lds + G::TILEB;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -408,13 +417,13 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(const AttnArgs a) 
       for (int st = 0; st < G::KS; ++st) s = mfma(row_frag<DP>(kt_lds, fo, b, st), qf[st], s);
 #pragma unroll
       for (int st = 0; st < G::KS; ++st) dp = mfma(row_frag<DP>(vt_lds, fo, b, st), gf[st], dp);
-      const bool edge = k0 + 32 * b + 31 > wq0;
+      if (k0 + 32 * b + 31 > wq0) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2));
-        s[r] = p * (dp[r] - delta);
-        if (edge && k0 + 32 * b + res_row(r, h) > q) s[r] = 0.f;
+        for (int r = 0; r < 16; ++r)
+          if (k0 + 32 * b + res_row(r, h) > q) s[r] = -kInf;
       }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
 #pragma unroll
       for (int s16 = 0; s16 < 2; ++s16) {
         const bf16x8_t ds = to_operand(s, s16);
@@ -430,21 +439,74 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(const AttnArgs a) 
 // One work-group: 128 key rows of one key head; the query and
 // upstream-gradient tiles of every query head of the group stream past, so
 // that the sums over rows and heads stay in registers, in a fixed order.
-// 8 waves, two per SIMD: wave w holds keys 32 (w & 3) .. + 31 and takes rows
-// 32 (w >> 2) .. + 31 of each 64-row tile; the two partial sums of a key are
-// joined through LDS at the end.
+//
+// 8 waves, two per SIMD.  Waves w and w + 4 hold the same 32 keys: each forms
+// p and ds of one half of a 64-row tile, then wave w sums dV over both halves
+// and wave w + 4 sums dK; what the other needs (ds of the first half, p of
+// the second) goes through LDS, 2 KB each way.  With half of the sums a wave
+// has registers to run ahead: in turn k it forms the scores of tile k, and
+// its exponentials run under the products of tile k - 1.  Three tiles in LDS:
+// k - 1 and k in use, k + 1 on its way.
 template <int DP>
 struct DkvLds {
-  static constexpr int ROWS = 2 * Geo<DP>::TILEB;             // q and dO tiles, then lse and delta
+  static constexpr int ROWS = 2 * Geo<DP>::TILEB;    // q and dO tiles, then lse and delta
   static constexpr int STAGE = ROWS + 2 * kAttnStep * 4;
-  static constexpr int JOIN = 4 * 64 * Geo<DP>::DB * 16 * 4;  // one accumulator of 4 waves
-  static constexpr int BYTES = 2 * STAGE > JOIN ? 2 * STAGE : JOIN;
+  static constexpr int MSG = 3 * STAGE;              // two turns of 8 waves' messages
+  static constexpr int BYTES = MSG + 2 * 8 * 2048;
 };
 
 // Four consecutive per-row values of a tile.
 __device__ __forceinline__ f32x4_t row_values(const LAS unsigned char* __restrict__ p) { return *(const LAS f32x4_t*)p; }
 
+// s = Q K^T and dp = dO V^T of row block b of a tile with the wave's keys.
 template <int DP>
+__device__ __forceinline__ void dkv_scores(const LAS unsigned char* __restrict__ tile, const FragOff& fo, int b,
+                                           const bf16x8_t (&kf)[Geo<DP>::KS], const bf16x8_t (&vf)[Geo<DP>::KS],
+                                           f32x16_t& s, f32x16_t& dp) {
+  s = dp = (f32x16_t)(0.f);
+#pragma unroll
+  for (int st = 0; st < Geo<DP>::KS; ++st) s = mfma(row_frag<DP>(tile, fo, b, st), kf[st], s);
+#pragma unroll
+  for (int st = 0; st < Geo<DP>::KS; ++st) dp = mfma(row_frag<DP>(tile + Geo<DP>::TILEB, fo, b, st), vf[st], dp);
+}
+
+// p in place of s and ds in place of dp.
+template <int DP>
+__device__ __forceinline__ void dkv_softmax(const LAS unsigned char* __restrict__ tile, int b, int h, float c,
+                                            f32x16_t& s, f32x16_t& dp) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const f32x4_t lse2 = row_values(tile + DkvLds<DP>::ROWS + (32 * b + 8 * g + 4 * h) * 4);
+    const f32x4_t delta = row_values(tile + DkvLds<DP>::ROWS + (kAttnStep + 32 * b + 8 * g + 4 * h) * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * g + i;
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2[i]));
+      dp[r] = s[r] * (dp[r] - delta[i]);
+    }
+  }
+}
+
+// acc += (rows of block b of a tile)^T x, x two operands of 16 rows.
+template <int DP>
+__device__ __forceinline__ void dkv_sums(const LAS unsigned char* __restrict__ tile, const FragOff& fo, int b,
+                                         const bf16x8_t (&x)[2], f32x16_t (&acc)[Geo<DP>::DB]) {
+#pragma unroll
+  for (int s16 = 0; s16 < 2; ++s16)
+#pragma unroll
+    for (int db = 0; db < Geo<DP>::DB; ++db) acc[db] = mfma(col_frag<DP>(tile, fo, db, 2 * b + s16), x[s16], acc[db]);
+}
+
+__device__ __forceinline__ void read_msg(const LAS unsigned char* __restrict__ p, bf16x8_t (&x)[2]) {
+  x[0] = *(const LAS bf16x8_t*)p;
+  x[1] = *(const LAS bf16x8_t*)(p + 1024);
+}
+__device__ __forceinline__ void write_msg(LAS unsigned char* __restrict__ p, const bf16x8_t (&x)[2]) {
+  *(LAS bf16x8_t*)p = x[0];
+  *(LAS bf16x8_t*)(p + 1024) = x[1];
+}
+
+template <int DP, bool EXACT>
 __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(const AttnArgs a) {
   using G = Geo<DP>;
   using L = DkvLds<DP>;
@@ -457,122 +519,132 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(const AttnArgs a)
   const int group = a.heads / a.kv_heads;
   const int nq = (t.len - t.first + kAttnStep - 1) / kAttnStep;  // query tiles from the diagonal on
   const int total = nq * group;
-  const int wk0 = t.first + 32 * (wave & 3), b = wave >> 2;
+  const int wk0 = t.first + 32 * (wave & 3), half = wave >> 2;
   const int key = wk0 + (lane & 31);
   const float c = a.scale * kLog2e;
 
-  const LoadLane qo = load_lane(lane, a.q.ts);
-  const LoadLane go = load_lane(lane, a.d_o.ts);
   const FragOff fo = frag_offsets(lane);
-  auto issue = [&](int it) {
-    LAS unsigned char* dst = lds + (it & 1) * L::STAGE;
-    const int head = kv * group + it / nq;
-    const int q0 = t.first + (it % nq) * kAttnStep;
-    const int64_t row = static_cast<int64_t>(t.row0) + q0;
-    load_tile<DP, 8>(a.q.p + (row * a.q.ts + head * a.q.hs) * 2, t.len - q0, a.q.ts, a.head_dim, qo, dst, wave);
-    load_tile<DP, 8>(a.d_o.p + (row * a.d_o.ts + head * a.d_o.hs) * 2, t.len - q0, a.d_o.ts, a.head_dim, go,
-                     dst + G::TILEB, wave);
-    if (wave < 2) {
-      const float* src = (wave == 0 ? a.row_lse2 : a.row_delta) + head * a.row_stride + row;
-      load_lds<true>(reinterpret_cast<const unsigned char*>(src), 4u * min(t.len - q0, kAttnStep), lane * 4,
-                     dst + L::ROWS + wave * kAttnStep * 4);
+  // From the sequence's last rows back to the diagonal, every head of the
+  // group in turn: work-groups of one key head, which share an XCD, then read
+  // the same tiles at about the same time.
+  int fill = 0, fill_row = t.first + (nq - 1) * kAttnStep, fill_head = 0;  // place, first row and head of the next load
+  const int64_t row_last = static_cast<int64_t>(t.row0) + fill_row;
+  TileLoad<DP, EXACT, 8> ql(a.q, row_last, kv * group, a.head_dim, wave, lane);
+  TileLoad<DP, EXACT, 8> gl(a.d_o, row_last, kv * group, a.head_dim, wave, lane);
+  const float* stat = (wave == 0 ? a.row_lse2 : a.row_delta) + kv * group * a.row_stride + row_last;
+  auto issue = [&]() {
+    LAS unsigned char* dst = lds + fill;
+    ql.load(t.len - fill_row, dst, wave);
+    gl.load(t.len - fill_row, dst + G::TILEB, wave);
+    if (wave < 2)
+      load_lds<true, 0>(reinterpret_cast<const unsigned char*>(stat), 4u * min(t.len - fill_row, kAttnStep), lane * 4,
+                        dst + L::ROWS + wave * kAttnStep * 4);
+    fill = fill == 2 * L::STAGE ? 0 : fill + L::STAGE;
+    int64_t heads = 1, rows = 0;
+    if (++fill_head == group) {
+      fill_head = 0;
+      fill_row -= kAttnStep;
+      heads = 1 - group;
+      rows = -kAttnStep;
     }
+    ql.move((heads * a.q.hs + rows * a.q.ts) * 2);
+    gl.move((heads * a.d_o.hs + rows * a.d_o.ts) * 2);
+    stat += heads * a.row_stride + rows;
   };
-  issue(0);
   const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
   bf16x8_t kf[G::KS], vf[G::KS];
   own_rows<DP>(a.k.p + (krow0 * a.k.ts + kv * a.k.hs) * 2, a.k.ts, a.head_dim, t.len - wk0, lane, kf);
   own_rows<DP>(a.v.p + (krow0 * a.v.ts + kv * a.v.hs) * 2, a.v.ts, a.head_dim, t.len - wk0, lane, vf);
-  f32x16_t dk[G::DB], dv[G::DB];
+  f32x16_t acc[G::DB];  // dV (first half of the waves) or dK
 #pragma unroll
-  for (int db = 0; db < G::DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
-
-  for (int it = 0; it < total; ++it) {
-    next_tile();
-    if (it + 1 < total) issue(it + 1);
-    const int qs = t.first + (it % nq) * kAttnStep + 32 * b;
-    if (qs + 31 < wk0 || qs >= t.len || wk0 >= t.len) continue;  // no query of the block sees a key of the wave
-    const LAS unsigned char* qt = lds + (it & 1) * L::STAGE;
-    const LAS unsigned char* gt = qt + G::TILEB;
-    f32x16_t s = (f32x16_t)(0.f), dp = (f32x16_t)(0.f);
+  for (int db = 0; db < G::DB; ++db) acc[db] = (f32x16_t)(0.f);
+  bf16x8_t own[2];
+  f32x16_t s, dp;
+  const int sum_of = half == 0 ? G::TILEB : 0;  // what the wave sums of a tile: dO or q
+  int cur = 0, turn = 0;  // the tile's place; 0 or 8 * 2048, where this turn's messages go
+  const int out = L::MSG + wave * 2048 + lane * 16, in = L::MSG + (wave ^ 4) * 2048 + lane * 16;
+  int qs = fill_row + 32 * half, head = 0;      // the wave's first row of the tile
+  auto mask = [&]() {
+    if (qs < wk0 + 31 || qs + 31 >= t.len) {
 #pragma unroll
-    for (int st = 0; st < G::KS; ++st) s = mfma(row_frag<DP>(qt, fo, b, st), kf[st], s);
-#pragma unroll
-    for (int st = 0; st < G::KS; ++st) dp = mfma(row_frag<DP>(gt, fo, b, st), vf[st], dp);
-    const bool edge = qs < wk0 + 31 || qs + 31 >= t.len;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f32x4_t lse2 = row_values(qt + L::ROWS + (32 * b + 8 * g + 4 * h) * 4);
-      const f32x4_t delta = row_values(qt + L::ROWS + (kAttnStep + 32 * b + 8 * g + 4 * h) * 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * g + i, q = qs + 8 * g + 4 * h + i;
-        float p = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2[i]));
-        float ds = p * (dp[r] - delta[i]);
-        if (edge && (key > q || q >= t.len)) p = ds = 0.f;
-        s[r] = p;
-        dp[r] = ds;
-      }
+      for (int r = 0; r < 16; ++r)
+        if (key > qs + res_row(r, h) || qs + res_row(r, h) >= t.len) s[r] = -kInf;
     }
-#pragma unroll
-    for (int s16 = 0; s16 < 2; ++s16) {
-      const bf16x8_t p = to_operand(s, s16), ds = to_operand(dp, s16);
-#pragma unroll
-      for (int db = 0; db < G::DB; ++db) dv[db] = mfma(col_frag<DP>(gt, fo, db, 2 * b + s16), p, dv[db]);
-#pragma unroll
-      for (int db = 0; db < G::DB; ++db) dk[db] = mfma(col_frag<DP>(qt, fo, db, 2 * b + s16), ds, dk[db]);
+    if (++head == group) {
+      head = 0;
+      qs -= kAttnStep;
     }
+  };
+  auto pass_on = [&]() {
+    const bf16x8_t p[2] = {to_operand(s, 0), to_operand(s, 1)}, ds[2] = {to_operand(dp, 0), to_operand(dp, 1)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) own[i] = half == 0 ? p[i] : ds[i];
+    const bf16x8_t other[2] = {half == 0 ? ds[0] : p[0], half == 0 ? ds[1] : p[1]};
+    write_msg(lds + out + turn, other);
+  };
+  issue();
+  next_tile();
+  if (total > 1) issue();
+  dkv_scores<DP>(lds + cur, fo, half, kf, vf, s, dp);
+  mask();
+  dkv_softmax<DP>(lds + cur, half, h, c, s, dp);
+  pass_on();
+  for (int it = 1; it < total; ++it) {
+    next_tile();  // tile `it` and the messages of turn it - 1 are there, tile it - 2 is done with
+    if (it + 1 < total) issue();
+    const int prev = cur + sum_of;
+    cur = cur == 2 * L::STAGE ? 0 : cur + L::STAGE;
+    turn ^= 8 * 2048;
+    dkv_scores<DP>(lds + cur, fo, half, kf, vf, s, dp);
+    mask();
+    bf16x8_t other[2];
+    read_msg(lds + in + (turn ^ (8 * 2048)), other);
+    dkv_sums<DP>(lds + prev, fo, half, own, acc);
+    dkv_softmax<DP>(lds + cur, half, h, c, s, dp);
+    dkv_sums<DP>(lds + prev, fo, half ^ 1, other, acc);
+    pass_on();
   }
-  // Waves 4..7 hand their sums to waves 0..3, dk first, then dv.
-  const bool live = key < t.len;
+  next_tile();
+  {
+    bf16x8_t other[2];
+    read_msg(lds + in + turn, other);
+    dkv_sums<DP>(lds + cur + sum_of, fo, half, own, acc);
+    dkv_sums<DP>(lds + cur + sum_of, fo, half ^ 1, other, acc);
+  }
   const int64_t row = static_cast<int64_t>(t.row0) + key;
-#pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    f32x16_t(&acc)[G::DB] = part == 0 ? dk : dv;
-    LAS float* at = (LAS float*)lds + ((wave & 3) * 64 + lane) * 4;
-    next_tile();
-    if (b == 1) {
-#pragma unroll
-      for (int db = 0; db < G::DB; ++db)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *(LAS f32x4_t*)(at + (db * 4 + g) * 1024) =
-              (f32x4_t){acc[db][4 * g], acc[db][4 * g + 1], acc[db][4 * g + 2], acc[db][4 * g + 3]};
-    }
-    next_tile();
-    if (b == 0) {
-#pragma unroll
-      for (int db = 0; db < G::DB; ++db)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x4_t o = *(const LAS f32x4_t*)(at + (db * 4 + g) * 1024);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[db][4 * g + i] += o[i];
-        }
-      store_rows<DP>(part == 0 ? a.dk : a.dv, row, kv, a.head_dim, live, lane, acc, part == 0 ? a.scale : 1.f);
-    }
-  }
+  store_rows<DP>(half == 0 ? a.dv : a.dk, row, kv, a.head_dim, key < t.len, lane, acc, half == 0 ? 1.f : a.scale);
+}
+
+}  // namespace
+
+namespace {
+
+template <int DP, bool EXACT>
+hipError_t forward(const AttnArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((attention_kernel<DP, EXACT>), dim3(static_cast<uint32_t>(a.n_tiles) * a.heads), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DP, bool EXACT>
+hipError_t backward(const AttnArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((attention_dq_kernel<DP, EXACT>), dim3(static_cast<uint32_t>(a.n_tiles) * a.heads), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attention_dkv_kernel<DP, EXACT>), dim3(static_cast<uint32_t>(a.n_tiles) * a.kv_heads), dim3(512), 0, s,
+                     a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_attention(const AttnArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<uint32_t>(a.n_tiles) * a.heads);
-  if (a.head_dim <= 64) hipLaunchKernelGGL(attention_kernel<64>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(attention_kernel<128>, grid, dim3(256), 0, s, a);
-  return hipGetLastError();
+  if (a.head_dim <= 64) return a.head_dim == 64 ? forward<64, true>(a, s) : forward<64, false>(a, s);
+  return a.head_dim == 128 ? forward<128, true>(a, s) : forward<128, false>(a, s);
 }
 
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s) {
-  const dim3 gq(static_cast<uint32_t>(a.n_tiles) * a.heads), gk(static_cast<uint32_t>(a.n_tiles) * a.kv_heads);
-  if (a.head_dim <= 64) {
-    hipLaunchKernelGGL(attention_dq_kernel<64>, gq, dim3(256), 0, s, a);
-    hipLaunchKernelGGL(attention_dkv_kernel<64>, gk, dim3(512), 0, s, a);
-  } else {
-    hipLaunchKernelGGL(attention_dq_kernel<128>, gq, dim3(256), 0, s, a);
-    hipLaunchKernelGGL(attention_dkv_kernel<128>, gk, dim3(512), 0, s, a);
-  }
-  return hipGetLastError();
+  if (a.head_dim <= 64) return a.head_dim == 64 ? backward<64, true>(a, s) : backward<64, false>(a, s);
+  return a.head_dim == 128 ? backward<128, true>(a, s) : backward<128, false>(a, s);
 }
 
 }  // namespace muon
