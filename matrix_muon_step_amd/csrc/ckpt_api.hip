@@ -80,6 +80,7 @@ muon_status_t move_all(const muon_checkpoint_t* items, int64_t n, bool write, vo
     d.tokens = static_cast<int32_t>(m.tokens);
     d.cols = static_cast<int32_t>(m.cols);
     d.blocks = static_cast<int32_t>(nS);
+    d.rblocks = static_cast<int32_t>(tiles(m.tokens, kCkTile));
     d.groups = static_cast<int32_t>(groups);
     d.f32 = m.x_dtype == MUON_F32;
     b.prefix[b.n + 1] = b.prefix[b.n] + work;
@@ -88,31 +89,65 @@ muon_status_t move_all(const muon_checkpoint_t* items, int64_t n, bool write, vo
   return flush();
 }
 
-// How a matrix's product is laid out: tiles of G, parts of the token range.
+// How a launch of gradients is laid out.
 struct GradPlan {
-  int64_t mt, nt, splits, per_split;
-  size_t part_bytes;
+  int cfg;
+  int64_t parts;   // 0: a work-group per tile
+  int64_t share;   // steps of a part
+  size_t bytes;    // of its pieces
 };
 
-GradPlan plan_grad(const muon_checkpoint_grad_t& m, int64_t call_tiles) {
-  GradPlan p;
-  p.mt = tiles(m.outs, kGradTile);
-  p.nt = tiles(m.cols, kGradTile);
-  const int64_t steps = tiles(m.tokens, 32);
-  // Calls with fewer tiles than the 256 compute units split the token range
-  // so that every unit has one, in parts of at least 16 steps.
-  int64_t want = std::max<int64_t>(1, 256 / std::max<int64_t>(1, call_tiles));
-  want = std::min(want, std::max<int64_t>(1, steps / 16));
-  p.per_split = std::max<int64_t>(1, tiles(steps, want));
-  p.splits = std::max<int64_t>(1, tiles(steps, p.per_split));
-  p.part_bytes = p.splits > 1 ? align_up(static_cast<size_t>(p.splits) * m.outs * m.cols * sizeof(float)) : 0;
-  return p;
-}
+constexpr int64_t kUnits = 256;  // compute units
 
-int64_t total_tiles(const muon_checkpoint_grad_t* mats, int64_t n) {
-  int64_t t = 0;
-  for (int64_t i = 0; i < n; ++i) t += tiles(mats[i].outs, kGradTile) * tiles(mats[i].cols, kGradTile);
-  return t;
+// The cheapest of three layouts, by what they measured (us; a step is 32
+// tokens of a tile):
+//   256-tiles, one work-group of 8 waves to a unit: 6 + 0.85 a step
+//     (1600 x 6400 from 16384 tokens, 175 tiles: 438)
+//   128-tiles, up to three work-groups of 4 waves to a unit, which together
+//     take 0.27 a step each: 8 + that (the same matrix, 650 tiles: 403; three
+//     1600 x 1600 from 8192 tokens, 507 tiles: 154 against 217 with 147
+//     256-tiles; but 2048 x 7168 from 777 tokens 40 against 30)
+//   the work in 256-tiles cut into equal shares, one to a unit: 1.0 a step
+//     with every unit busy, the pieces (256 KB each, written and read, at 4.5
+//     TB/s) and a second launch (1600 x 6400: 404)
+GradPlan plan_grad(const muon_checkpoint_grad_t* mats, int64_t n) {
+  int64_t tiles_of[kNumGradCfg] = {0, 0}, work[kNumGradCfg] = {0, 0}, longest = 0;
+  bool empty = false;
+  for (int64_t i = 0; i < n; ++i) {
+    const int64_t steps = tiles(mats[i].tokens, kCkTile);
+    longest = std::max(longest, steps);
+    empty = empty || steps == 0;
+    for (int c = 0; c < kNumGradCfg; ++c) {
+      const int64_t t = tiles(mats[i].outs, kGradTile[c]) * tiles(mats[i].cols, kGradTile[c]);
+      tiles_of[c] += t;
+      work[c] += t * steps;
+    }
+  }
+  // Rounds of items over the units, of items of average length or one of the longest.
+  auto whole = [&](int c, double start, int64_t together, double step) {
+    const int64_t count = std::max<int64_t>(1, tiles_of[c]);
+    const double steps = static_cast<double>(tiles(tiles_of[c], kUnits)) * work[c] / count;
+    return start * tiles(count, together * kUnits) + step * std::max(static_cast<double>(longest), steps);
+  };
+  const double t256 = whole(kGrad256, 6, 1, 0.85), t128 = whole(kGrad128, 8, 3, 0.27);
+  const int64_t parts = std::min(kUnits, work[kGrad256] / 16);
+  GradPlan p = {t256 <= t128 ? kGrad256 : kGrad128, 0, 0, 0};
+  if (parts > 1) {
+    const double pieces = static_cast<double>(parts + std::min<int64_t>(parts, tiles_of[kGrad256]));
+    const double cut = 6 + 1.0 * tiles(work[kGrad256], parts) + pieces * 0.524 / 4.5 + 5.0;
+    if (cut < std::min(t256, t128)) {
+      p.cfg = kGrad256;
+      p.share = tiles(work[kGrad256], parts);
+      p.parts = tiles(work[kGrad256], p.share);
+    }
+  }
+  if (empty && p.parts == 0) {  // tiles without steps are written by the joining pass
+    p.cfg = kGrad256;
+    p.share = std::max<int64_t>(1, tiles(work[kGrad256], kUnits));
+    p.parts = std::max<int64_t>(1, tiles(work[kGrad256], p.share));
+  }
+  if (p.parts) p.bytes = align_up(static_cast<size_t>(p.parts) * 2 * kGradTile[p.cfg] * kGradTile[p.cfg] * sizeof(float));
+  return p;
 }
 
 muon_status_t check_grads(const muon_checkpoint_grad_t* mats, int64_t n) {
@@ -162,8 +197,8 @@ size_t muon_checkpoint_grad_workspace_bytes(const muon_checkpoint_grad_t* mats, 
   guarded([&] {
     const muon_status_t st = check_grads(mats, n);
     if (st != MUON_OK) return st;
-    const int64_t all = total_tiles(mats, n);
-    for (int64_t i = 0; i < n; ++i) bytes += plan_grad(mats[i], all).part_bytes;
+    for (int64_t i = 0; i < n; i += kGradBatch)
+      bytes = std::max(bytes, plan_grad(mats + i, std::min<int64_t>(kGradBatch, n - i)).bytes);
     return MUON_OK;
   });
   return bytes;
@@ -174,15 +209,13 @@ muon_status_t muon_checkpoint_grad(const muon_checkpoint_grad_t* mats, int64_t n
   return guarded([&]() -> muon_status_t {
     muon_status_t st = check_grads(mats, n);
     if (st != MUON_OK) return st;
-    const int64_t all = total_tiles(mats, n);
-    std::vector<GradPlan> plans;
     std::vector<Range> rs;
     size_t need = 0;
+    for (int64_t i = 0; i < n; i += kGradBatch)
+      need = std::max(need, plan_grad(mats + i, std::min<int64_t>(kGradBatch, n - i)).bytes);
     for (int64_t i = 0; i < n; ++i) {
       const muon_checkpoint_grad_t& m = mats[i];
       const std::string id = "muon: gradient " + std::to_string(i);
-      plans.push_back(plan_grad(m, all));
-      need += plans.back().part_bytes;
       if (!m.G || (m.tokens > 0 && (!m.dy || !m.data)))
         return fail(MUON_ERR_INVALID_ARG, id + " has a NULL dy, data or G");
       const uintptr_t dy = reinterpret_cast<uintptr_t>(m.dy), p = reinterpret_cast<uintptr_t>(m.data);
@@ -206,56 +239,44 @@ muon_status_t muon_checkpoint_grad(const muon_checkpoint_grad_t* mats, int64_t n
     st = check_aliasing(rs);
     if (st != MUON_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    unsigned char* part = static_cast<unsigned char*>(workspace);
-    // Two kinds of launches: dY read in 16-byte direct loads, or any way.
-    std::vector<unsigned char*> parts(n);
-    for (int64_t i = 0; i < n; ++i) {
-      parts[i] = part;
-      part += plans[i].part_bytes;
-    }
-    for (int kind = 0; kind < 2; ++kind) {
+    // Launches follow one another on the stream and share the workspace.
+    for (int64_t i0 = 0; i0 < n; i0 += kGradBatch) {
+      const int64_t count = std::min<int64_t>(kGradBatch, n - i0);
+      const GradPlan plan = plan_grad(mats + i0, count);
       GradBatch b;
       memset(&b, 0, sizeof(b));
-      auto flush = [&]() -> muon_status_t {
-        if (b.n == 0) return MUON_OK;
-        hipError_t e = launch_ckpt_grad(b, kind == 0, s);
-        if (e == hipSuccess && b.sums[b.n] > 0) e = launch_grad_join(b, s);
-        memset(&b, 0, sizeof(b));
-        return e == hipSuccess ? MUON_OK : hip_fail(e, "gradient launch");
-      };
-      for (int64_t i = 0; i < n; ++i) {
+      b.parts = static_cast<int32_t>(plan.parts);
+      b.share = plan.share;
+      b.pieces = static_cast<float*>(workspace);
+      bool aligned = true;
+      for (int64_t i = i0; i < i0 + count; ++i) {
         const muon_checkpoint_grad_t& m = mats[i];
-        const bool aligned = reinterpret_cast<uintptr_t>(m.dy) % 16 == 0 && m.dy_stride % 8 == 0;
-        if (aligned != (kind == 0)) continue;
         if (m.tokens == 0 && m.accumulate) continue;
-        const GradPlan& p = plans[i];
+        aligned = aligned && reinterpret_cast<uintptr_t>(m.dy) % 16 == 0 && m.dy_stride % 8 == 0;
         GradDesc& d = b.d[b.n];
         d.dy = static_cast<const unsigned char*>(m.dy);
         d.dy_stride = m.dy_stride;
         d.codes = static_cast<const unsigned char*>(m.data);
         d.exps = d.codes + blocks_of(m.tokens, m.cols) * kCkBlockBytes;
         d.G = static_cast<unsigned char*>(m.G);
-        d.part = reinterpret_cast<float*>(parts[i]);
         d.tokens = static_cast<int32_t>(m.tokens);
         d.outs = static_cast<int32_t>(m.outs);
         d.cols = static_cast<int32_t>(m.cols);
         d.blocks = static_cast<int32_t>(tiles(m.cols, kCkTile));
-        d.mt = static_cast<int32_t>(p.mt);
-        d.nt = static_cast<int32_t>(p.nt);
-        d.splits = static_cast<int32_t>(p.splits);
-        d.per_split = static_cast<int32_t>(p.per_split);
+        d.mt = static_cast<int32_t>(tiles(m.outs, kGradTile[plan.cfg]));
+        d.steps = static_cast<int32_t>(tiles(m.tokens, kCkTile));
         d.g_f32 = m.g_dtype == MUON_F32;
         d.accumulate = m.accumulate;
-        b.prefix[b.n + 1] = b.prefix[b.n] + static_cast<int32_t>(p.mt * p.nt * p.splits);
-        b.sums[b.n + 1] =
-            b.sums[b.n] + (p.splits > 1 ? static_cast<int32_t>(tiles(m.outs * m.cols, kGradSumElems)) : 0);
-        if (++b.n == kGradBatch) {
-          st = flush();
-          if (st != MUON_OK) return st;
-        }
+        const int64_t t = d.mt * tiles(m.cols, kGradTile[plan.cfg]);
+        b.tiles[b.n + 1] = b.tiles[b.n] + static_cast<int32_t>(t);
+        b.steps[b.n + 1] = b.steps[b.n] + t * d.steps;
+        ++b.n;
       }
-      st = flush();
-      if (st != MUON_OK) return st;
+      if (b.n == 0) continue;
+      hipError_t e = hipSuccess;
+      if (b.parts == 0 || b.steps[b.n] > 0) e = launch_ckpt_grad(b, plan.cfg, aligned, s);
+      if (e == hipSuccess && b.parts) e = launch_grad_join(b, s);
+      if (e != hipSuccess) return hip_fail(e, "gradient launch");
     }
     return MUON_OK;
   });
