@@ -333,7 +333,7 @@ muon_status_t muon_qk_clip(const muon_qk_clip_matrix_t* mats, int64_t n, float t
 
 /* A packing: sequences of the given lengths laid end to end in the first
  * sum(lengths) rows of the token dimension.  muon_packing_create checks the
- * lengths (each >= 0; sum <= MUON_MAX_TOKENS) and writes the kernels' work
+ * lengths (each 0 .. MUON_MAX_SEQUENCE; sum <= MUON_MAX_TOKENS) and writes the kernels' work
  * list into `table` (DEVICE, muon_packing_bytes bytes, 256-byte aligned)
  * through `stream`, which it synchronises; the handle may then be used on any
  * stream of that device, by any number of calls at once.  The caller keeps
@@ -342,6 +342,7 @@ muon_status_t muon_qk_clip(const muon_qk_clip_matrix_t* mats, int64_t n, float t
  * does not wait.  Zero sequences, and empty ones, are allowed.
  * muon_packing_bytes returns 0 on invalid lengths. */
 #define MUON_MAX_TOKENS 1073741824
+#define MUON_MAX_SEQUENCE 16777216
 typedef struct muon_packing_s* muon_packing_t;
 size_t muon_packing_bytes(const int64_t* lengths, int64_t n);
 muon_status_t muon_packing_create(const int64_t* lengths, int64_t n, void* table, size_t table_bytes, void* stream,
@@ -380,7 +381,8 @@ typedef struct muon_heads {
  *              starts it at -infinity).  logit_heads is heads or kv_heads:
  *              the latter is what muon_qk_clip takes for a grouped layout
  *              (query projection with head_dim * heads / kv_heads rows per
- *              entry, key projection with head_dim).  NaN logits give NaN.
+ *              entry, key projection with head_dim).  A NaN logit gives
+ *              NaN, +infinity where the row's largest logit is that.
  *   heads      a multiple of kv_heads >= 1, at most MUON_MAX_HEADS
  *   head_dim   a multiple of 8, 8..128 (others: MUON_ERR_UNSUPPORTED)
  *   scale      finite, > 0

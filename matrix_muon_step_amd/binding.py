@@ -360,6 +360,9 @@ def _on(device, stream):
     allocations made for the call belong to that stream); yields the stream."""
     import torch
 
+    if stream is None and (device is None or device.index == torch.cuda.current_device()):
+        yield torch.cuda.current_stream()  # already current: nothing to enter
+        return
     if device is None:
         st = _torch_stream(stream)
         with torch.cuda.stream(st):
@@ -668,9 +671,10 @@ class MuonPacking:
     layer of a batch, forward and backward, on any stream of its device.  Keep
     it alive as long as a graph that was captured with it is replayed."""
 
-    def __init__(self, handle, lengths, table, device):
+    def __init__(self, handle, lengths, table, device, stream):
         self._h = handle
         self._table = table
+        self._stream = stream  # the table's memory belongs to it
         self.lengths = tuple(lengths)
         self.tokens = sum(lengths)
         self.device = device
@@ -682,7 +686,8 @@ class MuonPacking:
             raise RuntimeError("the packing is closed")
         if device is not None and device != self.device:
             raise ValueError(f"the packing is on {self.device}, the call's tensors on {device}")
-        self._table.record_stream(stream)
+        if stream.cuda_stream != self._stream:
+            self._table.record_stream(stream)
         return ctypes.c_void_p(self._h)
 
     def close(self) -> None:
@@ -717,26 +722,26 @@ def muon_packing_create(lengths: Sequence[int], device=None, stream=None) -> Muo
         h = ctypes.c_void_p()
         _check(lib().muon_packing_create(arr, len(lengths), ctypes.c_void_p(table.data_ptr()), need,
                                          ctypes.c_void_p(st.cuda_stream), ctypes.byref(h)))
-    return MuonPacking(h.value, lengths, table, device)
+    return MuonPacking(h.value, lengths, table, device, st.cuda_stream)
 
 
 def _heads_tensor(name, t, rows, device, like=None):
     """Checks a (rows, heads, head_dim) bfloat16 tensor; returns its muon_heads_t and the call's device."""
     import torch
 
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
+    shape = t.shape
+    if not t.is_cuda or t.dtype != torch.bfloat16 or len(shape) != 3:
         raise ValueError(f"{name} must be a bfloat16 GPU tensor (tokens, heads, head_dim)")
     device = _same_device(device, t, name)
-    if t.shape[0] != rows:
-        raise ValueError(f"{name} has {t.shape[0]} rows, the call {rows}")
-    if like is not None and t.shape != like.shape:
+    if shape[0] != rows:
+        raise ValueError(f"{name} has {shape[0]} rows, the call {rows}")
+    if like is not None and shape != like.shape:
         raise ValueError(f"{name} must have the shape {tuple(like.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    ts, hs, ds = t.stride()
+    if shape[2] > 1 and ds != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     # the stride of a dimension of size one says nothing
-    ts = t.stride(0) if t.shape[0] > 1 else 0
-    hs = t.stride(1) if t.shape[1] > 1 else 0
-    return muon_heads_t(t.data_ptr(), ts, hs), device
+    return muon_heads_t(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0), device
 
 
 def _attention_rows(q, k, v, packing):

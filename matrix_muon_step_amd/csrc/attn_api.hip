@@ -37,6 +37,8 @@ muon_status_t count_tiles(const int64_t* lengths, int64_t n, int64_t* tokens, in
   int64_t sum = 0, count = 0;
   for (int64_t i = 0; i < n; ++i) {
     if (lengths[i] < 0) return fail(MUON_ERR_INVALID_ARG, "muon: packing length " + std::to_string(i) + " is negative");
+    if (lengths[i] > MUON_MAX_SEQUENCE)
+      return fail(MUON_ERR_UNSUPPORTED, "muon: packing length " + std::to_string(i) + " exceeds MUON_MAX_SEQUENCE");
     if (lengths[i] > MUON_MAX_TOKENS - sum)
       return fail(MUON_ERR_UNSUPPORTED, "muon: a packing holds at most MUON_MAX_TOKENS tokens");
     sum += lengths[i];

@@ -332,11 +332,13 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(const AttnArgs a) {
   const bool live = q < t.len;
   l = half_sum(l);
   store_rows<DP>(a.o, static_cast<int64_t>(t.row0) + q, head, a.head_dim, live, lane, o, 1.f / l);
-  if (live && h == 0)
-    gst(a.lse + head * a.lse_stride + t.row0 + q, fmaf(m_ref, a.scale, kLn2 * __builtin_amdgcn_logf(l)));
+  if (live && h == 0) {
+    const float ref = m_ref == -kInf ? 0.f : m_ref * c;  // as the exponentials had it
+    gst(a.lse + head * a.lse_stride + t.row0 + q, (ref + __builtin_amdgcn_logf(l)) * kLn2);
+  }
   if (a.max_logit) {
-    // A row whose sum is NaN has a NaN logit (or only infinite ones).
-    float top = !live ? -kInf : l != l ? __builtin_nanf("") : m_top * a.scale;
+    // A row whose sum is NaN has an infinite logit, or else a NaN.
+    float top = !live ? -kInf : l != l && m_top < kInf ? __builtin_nanf("") : m_top * a.scale;
 #pragma unroll
     for (int off = 1; off <= 16; off <<= 1) {
       const float other = __shfl_xor(top, off, 64);
