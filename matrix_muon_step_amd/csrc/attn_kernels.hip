@@ -187,8 +187,22 @@ __device__ __forceinline__ void next_tile() {
   asm volatile("" ::: "memory");
 }
 
-__device__ __forceinline__ float half_max(float x) { return fmaxf(x, __shfl_xor(x, 32, 64)); }
-__device__ __forceinline__ float half_sum(float x) { return x + __shfl_xor(x, 32, 64); }
+// x of lane l and of lane l ^ 32, the lower lane's first.
+__device__ __forceinline__ void halves(float x, float& lo, float& hi) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  lo = __uint_as_float(r[0]);
+  hi = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float half_max(float x) {
+  float a, b;
+  halves(x, a, b);
+  return fmaxf(a, b);
+}
+__device__ __forceinline__ float half_sum(float x) {
+  float a, b;
+  halves(x, a, b);
+  return a + b;
+}
 
 // Right operands of the rows that a wave owns, straight from global memory:
 // row (lane & 31) of the wave's 32, all k-steps.  Rows at or past `rows` and
@@ -231,8 +245,11 @@ __device__ __forceinline__ void store_rows(const HeadsView& v, int64_t row, int 
 // Running maximum of a float in memory, in any order of arrival with the
 // same result: for values >= 0 the integer order of the bits is the float
 // order, for negative ones the reverse.  NaN is passed as 0x7fffffff, which
-// both orders keep.
+// both orders keep.  The value only grows, so one that is seen to have it
+// already (even an old one) needs no atomic: without that look, the 3800
+// atomics of a 4100-token call on 25 neighbouring floats cost 15 of its 42 us.
 __device__ __forceinline__ void atomic_max_float(float* p, float x) {
+  if (x <= __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) return;
   const int b = x != x ? 0x7fffffff : __float_as_int(x);
   if (b >= 0) atomicMax(reinterpret_cast<int*>(p), b);
   else atomicMin(reinterpret_cast<unsigned int*>(p), static_cast<unsigned int>(b));
@@ -242,7 +259,7 @@ __device__ __forceinline__ void atomic_max_float(float* p, float x) {
 // One work-group: 128 query rows of one head, 4 waves of 32 rows; key and
 // value tiles of 64 rows stream through a double buffer in LDS.
 template <int DP, bool EXACT>
-__global__ __launch_bounds__(256, 2) void attention_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attention_kernel(const AttnArgs a) {
   using G = Geo<DP>;
   __shared__ __align__(1024) unsigned char smem[4 * G::TILEB];
   LAS unsigned char* lds = (LAS unsigned char*)smem;
@@ -282,7 +299,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(const AttnArgs a) {
     const int k0 = kt * kAttnStep, cur = fill ^ (2 * G::TILEB);
     next_tile();
     if (kt + 1 < nk) issue();
-    if (k0 > wq0 + 31) continue;  // every key lies behind the wave's rows
+    if (k0 > wq0 + 31 || wq0 >= t.len) continue;  // every key lies behind the wave's rows, or it has none
     const LAS unsigned char* kt_lds = lds + cur;
     const LAS unsigned char* vt_lds = kt_lds + G::TILEB;
     f32x16_t s[2];
@@ -353,7 +370,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(const AttnArgs a) {
 // value tiles stream past.  Also forms delta and leaves it, with lse in
 // base 2, for the dK/dV kernel that follows.
 template <int DP, bool EXACT>
-__global__ __launch_bounds__(256, 2) void attention_dq_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attention_dq_kernel(const AttnArgs a) {
   using G = Geo<DP>;
   __shared__ __align__(1024) unsigned char smem[4 * G::TILEB];
   LAS unsigned char* lds = (LAS unsigned char*)smem;
@@ -409,7 +426,7 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(const AttnArgs a) 
     const int k0 = kt * kAttnStep, cur = fill ^ (2 * G::TILEB);
     next_tile();
     if (kt + 1 < nk) issue();
-    if (k0 > wq0 + 31) continue;
+    if (k0 > wq0 + 31 || wq0 >= t.len) continue;
     const LAS unsigned char* kt_lds = lds + cur;
     const LAS unsigned char* vt_lds = kt_lds + G::TILEB;
 #pragma unroll
@@ -508,8 +525,59 @@ __device__ __forceinline__ void write_msg(LAS unsigned char* __restrict__ p, con
   *(LAS bf16x8_t*)(p + 1024) = x[1];
 }
 
+// The tiles that stream past a key tile: from the sequence's last rows back to
+// the diagonal, every query head of the group in turn, so that work-groups of
+// one key head read the same tiles at about the same time.
+template <int DP, bool EXACT, int NW>
+struct QueryStream {
+  using L = DkvLds<DP>;
+  TileLoad<DP, EXACT, NW> ql, gl;
+  const float* stat;           // this wave's statistic: lse (wave 0) or delta (wave 1)
+  int64_t stat_stride;
+  int64_t q_head, q_back, g_head, g_back;  // bytes to the next head; from the last head to the first, a tile back
+  int row, head, group;        // first row and head of the next tile
+  int fill;                    // its place in LDS
+  __device__ __forceinline__ QueryStream(const AttnArgs& a, const AttnTile& t, int kv, int nq, int wave, int lane)
+      : ql(a.q, t.row0 + static_cast<int64_t>(t.first) + (nq - 1) * kAttnStep, kv * (a.heads / a.kv_heads), a.head_dim, wave,
+           lane),
+        gl(a.d_o, t.row0 + static_cast<int64_t>(t.first) + (nq - 1) * kAttnStep, kv * (a.heads / a.kv_heads), a.head_dim,
+           wave, lane) {
+    group = a.heads / a.kv_heads;
+    row = t.first + (nq - 1) * kAttnStep;
+    head = fill = 0;
+    stat = (wave == 0 ? a.row_lse2 : a.row_delta) + kv * group * a.row_stride + t.row0 + row;
+    stat_stride = a.row_stride;
+    q_head = a.q.hs * 2;
+    g_head = a.d_o.hs * 2;
+    q_back = -((group - 1) * a.q.hs + kAttnStep * a.q.ts) * 2;
+    g_back = -((group - 1) * a.d_o.hs + kAttnStep * a.d_o.ts) * 2;
+  }
+  // Starts this wave's loads of the next of RING tiles.
+  template <int RING>
+  __device__ __forceinline__ void next(int len, LAS unsigned char* lds, int wave, int lane) {
+    LAS unsigned char* dst = lds + fill;
+    ql.load(len - row, dst, wave);
+    gl.load(len - row, dst + Geo<DP>::TILEB, wave);
+    if (wave < 2)
+      load_lds<true, 0>(reinterpret_cast<const unsigned char*>(stat), 4u * min(len - row, kAttnStep), lane * 4,
+                        dst + L::ROWS + wave * kAttnStep * 4);
+    fill = fill == (RING - 1) * L::STAGE ? 0 : fill + L::STAGE;
+    if (++head == group) {
+      head = 0;
+      row -= kAttnStep;
+      ql.move(q_back);
+      gl.move(g_back);
+      stat -= (group - 1) * stat_stride + kAttnStep;
+    } else {
+      ql.move(q_head);
+      gl.move(g_head);
+      stat += stat_stride;
+    }
+  }
+};
+
 template <int DP, bool EXACT>
-__global__ __launch_bounds__(512, 2) void attention_dkv_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnArgs a) {
   using G = Geo<DP>;
   using L = DkvLds<DP>;
   __shared__ __align__(1024) unsigned char smem[L::BYTES];
@@ -526,33 +594,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(const AttnArgs a)
   const float c = a.scale * kLog2e;
 
   const FragOff fo = frag_offsets(lane);
-  // From the sequence's last rows back to the diagonal, every head of the
-  // group in turn: work-groups of one key head, which share an XCD, then read
-  // the same tiles at about the same time.
-  int fill = 0, fill_row = t.first + (nq - 1) * kAttnStep, fill_head = 0;  // place, first row and head of the next load
-  const int64_t row_last = static_cast<int64_t>(t.row0) + fill_row;
-  TileLoad<DP, EXACT, 8> ql(a.q, row_last, kv * group, a.head_dim, wave, lane);
-  TileLoad<DP, EXACT, 8> gl(a.d_o, row_last, kv * group, a.head_dim, wave, lane);
-  const float* stat = (wave == 0 ? a.row_lse2 : a.row_delta) + kv * group * a.row_stride + row_last;
-  auto issue = [&]() {
-    LAS unsigned char* dst = lds + fill;
-    ql.load(t.len - fill_row, dst, wave);
-    gl.load(t.len - fill_row, dst + G::TILEB, wave);
-    if (wave < 2)
-      load_lds<true, 0>(reinterpret_cast<const unsigned char*>(stat), 4u * min(t.len - fill_row, kAttnStep), lane * 4,
-                        dst + L::ROWS + wave * kAttnStep * 4);
-    fill = fill == 2 * L::STAGE ? 0 : fill + L::STAGE;
-    int64_t heads = 1, rows = 0;
-    if (++fill_head == group) {
-      fill_head = 0;
-      fill_row -= kAttnStep;
-      heads = 1 - group;
-      rows = -kAttnStep;
-    }
-    ql.move((heads * a.q.hs + rows * a.q.ts) * 2);
-    gl.move((heads * a.d_o.hs + rows * a.d_o.ts) * 2);
-    stat += heads * a.row_stride + rows;
-  };
+  QueryStream<DP, EXACT, 8> stream(a, t, kv, nq, wave, lane);
   const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
   bf16x8_t kf[G::KS], vf[G::KS];
   own_rows<DP>(a.k.p + (krow0 * a.k.ts + kv * a.k.hs) * 2, a.k.ts, a.head_dim, t.len - wk0, lane, kf);
@@ -565,7 +607,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(const AttnArgs a)
   const int sum_of = half == 0 ? G::TILEB : 0;  // what the wave sums of a tile: dO or q
   int cur = 0, turn = 0;  // the tile's place; 0 or 8 * 2048, where this turn's messages go
   const int out = L::MSG + wave * 2048 + lane * 16, in = L::MSG + (wave ^ 4) * 2048 + lane * 16;
-  int qs = fill_row + 32 * half, head = 0;      // the wave's first row of the tile
+  int qs = stream.row + 32 * half, head = 0;  // the wave's first row of the tile
   auto mask = [&]() {
     if (qs < wk0 + 31 || qs + 31 >= t.len) {
 #pragma unroll
@@ -584,16 +626,16 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(const AttnArgs a)
     const bf16x8_t other[2] = {half == 0 ? ds[0] : p[0], half == 0 ? ds[1] : p[1]};
     write_msg(lds + out + turn, other);
   };
-  issue();
+  stream.template next<3>(t.len, lds, wave, lane);
   next_tile();
-  if (total > 1) issue();
+  if (total > 1) stream.template next<3>(t.len, lds, wave, lane);
   dkv_scores<DP>(lds + cur, fo, half, kf, vf, s, dp);
   mask();
   dkv_softmax<DP>(lds + cur, half, h, c, s, dp);
   pass_on();
   for (int it = 1; it < total; ++it) {
     next_tile();  // tile `it` and the messages of turn it - 1 are there, tile it - 2 is done with
-    if (it + 1 < total) issue();
+    if (it + 1 < total) stream.template next<3>(t.len, lds, wave, lane);
     const int prev = cur + sum_of;
     cur = cur == 2 * L::STAGE ? 0 : cur + L::STAGE;
     turn ^= 8 * 2048;
@@ -617,6 +659,67 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_kernel(const AttnArgs a)
   store_rows<DP>(half == 0 ? a.dv : a.dk, row, kv, a.head_dim, key < t.len, lane, acc, half == 0 ? 1.f : a.scale);
 }
 
+// The same for head dimensions up to 64: 4 waves of 32 keys that each take all
+// rows of a tile and both sums, which fits 168 registers, and two tiles in
+// LDS, so that three work-groups share a unit (the pair kernel's 83 KB leave
+// room for one, and its start and end, about 6 us, lie open: 64 sequences of
+// 64 tokens and 25 heads took 52 us with dQ, 30 with this).
+template <int DP, bool EXACT>
+__global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a) {
+  using G = Geo<DP>;
+  using L = DkvLds<DP>;
+  __shared__ __align__(1024) unsigned char smem[2 * L::STAGE];
+  LAS unsigned char* lds = (LAS unsigned char*)smem;
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kv = blockIdx.x % a.kv_heads;
+  const AttnTile t = a.by_key[blockIdx.x / a.kv_heads];
+  const int nq = (t.len - t.first + kAttnStep - 1) / kAttnStep;  // query tiles from the diagonal on
+  const int total = nq * (a.heads / a.kv_heads);
+  const int wk0 = t.first + 32 * wave;
+  const int key = wk0 + (lane & 31);
+  const float c = a.scale * kLog2e;
+  const FragOff fo = frag_offsets(lane);
+  QueryStream<DP, EXACT, 4> stream(a, t, kv, nq, wave, lane);
+  int q0 = stream.row, head = 0, cur = 0;
+  stream.template next<2>(t.len, lds, wave, lane);
+  const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
+  bf16x8_t kf[G::KS], vf[G::KS];
+  own_rows<DP>(a.k.p + (krow0 * a.k.ts + kv * a.k.hs) * 2, a.k.ts, a.head_dim, t.len - wk0, lane, kf);
+  own_rows<DP>(a.v.p + (krow0 * a.v.ts + kv * a.v.hs) * 2, a.v.ts, a.head_dim, t.len - wk0, lane, vf);
+  f32x16_t dk[G::DB], dv[G::DB];
+#pragma unroll
+  for (int db = 0; db < G::DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
+  for (int it = 0; it < total; ++it) {
+    next_tile();
+    if (it + 1 < total) stream.template next<2>(t.len, lds, wave, lane);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int qs = q0 + 32 * b;
+      if (qs + 31 < wk0 || qs >= t.len || wk0 >= t.len) continue;  // no query of the block sees a key of the wave
+      f32x16_t s, dp;
+      dkv_scores<DP>(lds + cur, fo, b, kf, vf, s, dp);
+      if (qs < wk0 + 31 || qs + 31 >= t.len) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (key > qs + res_row(r, h) || qs + res_row(r, h) >= t.len) s[r] = -kInf;
+      }
+      dkv_softmax<DP>(lds + cur, b, h, c, s, dp);
+      const bf16x8_t p[2] = {to_operand(s, 0), to_operand(s, 1)}, ds[2] = {to_operand(dp, 0), to_operand(dp, 1)};
+      dkv_sums<DP>(lds + cur + G::TILEB, fo, b, p, dv);
+      dkv_sums<DP>(lds + cur, fo, b, ds, dk);
+    }
+    cur = L::STAGE - cur;
+    if (++head == stream.group) {
+      head = 0;
+      q0 -= kAttnStep;
+    }
+  }
+  const int64_t row = static_cast<int64_t>(t.row0) + key;
+  store_rows<DP>(a.dk, row, kv, a.head_dim, key < t.len, lane, dk, a.scale);
+  store_rows<DP>(a.dv, row, kv, a.head_dim, key < t.len, lane, dv, 1.f);
+}
+
 }  // namespace
 
 namespace {
@@ -632,8 +735,9 @@ hipError_t backward(const AttnArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((attention_dq_kernel<DP, EXACT>), dim3(static_cast<uint32_t>(a.n_tiles) * a.heads), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attention_dkv_kernel<DP, EXACT>), dim3(static_cast<uint32_t>(a.n_tiles) * a.kv_heads), dim3(512), 0, s,
-                     a);
+  const dim3 grid(static_cast<uint32_t>(a.n_tiles) * a.kv_heads);
+  if constexpr (DP == 64) hipLaunchKernelGGL((attention_dkv_kernel<DP, EXACT>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((attention_dkv_pair_kernel<DP, EXACT>), grid, dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
