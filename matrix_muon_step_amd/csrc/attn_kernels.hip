@@ -659,11 +659,11 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
   store_rows<DP>(half == 0 ? a.dv : a.dk, row, kv, a.head_dim, key < t.len, lane, acc, half == 0 ? 1.f : a.scale);
 }
 
-// The same for head dimensions up to 64: 4 waves of 32 keys that each take all
-// rows of a tile and both sums, which fits 168 registers, and two tiles in
-// LDS, so that three work-groups share a unit (the pair kernel's 83 KB leave
-// room for one, and its start and end, about 6 us, lie open: 64 sequences of
-// 64 tokens and 25 heads took 52 us with dQ, 30 with this).
+// The same for head dimensions up to 64 and many key tiles: 4 waves of 32 keys
+// that each take all rows of a tile and both sums, which fits 168 registers,
+// and two tiles in LDS, so that three work-groups share a unit (the pair
+// kernel's 83 KB leave room for one, whose start and end, about 6 us, lie
+// open).
 template <int DP, bool EXACT>
 __global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a) {
   using G = Geo<DP>;
@@ -736,7 +736,12 @@ hipError_t backward(const AttnArgs& a, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 grid(static_cast<uint32_t>(a.n_tiles) * a.kv_heads);
-  if constexpr (DP == 64) hipLaunchKernelGGL((attention_dkv_kernel<DP, EXACT>), grid, dim3(256), 0, s, a);
+  // Up to two key tiles for each of the 256 compute units, the longest one's
+  // turns are what takes the time, and the pair kernel's are half as long;
+  // with more the three-to-a-unit kernel wins.  dQ, dK and dV with heads of 64,
+  // us, pair | three: 1290 tokens, 25 heads (275 tiles) 58 | 71; 8 x 512
+  // (800) 70 | 51; 4096 (800) 272 | 253; 64 x 64 (1600) 52 | 37.
+  if (DP == 64 && grid.x > 512) hipLaunchKernelGGL((attention_dkv_kernel<64, EXACT>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((attention_dkv_pair_kernel<DP, EXACT>), grid, dim3(512), 0, s, a);
   return hipGetLastError();
 }

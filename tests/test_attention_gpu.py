@@ -117,6 +117,14 @@ def test_layouts(mm, heads, kv_heads, dim, layout):
     check_backward(mm, [70, 1, 150], heads, kv_heads, dim, layout=layout)
 
 
+def test_many_tiles(mm):
+    """More key tiles than the pair kernel takes (heads of 64 and fewer)."""
+    lengths = [1, 130, 40, 0, 257, 64, 128, 33] * 6
+    check_forward(mm, lengths, 10, 10, 64)
+    check_backward(mm, lengths, 10, 10, 64, behind=2)
+    check_backward(mm, lengths, 16, 8, 40)
+
+
 def test_long_sequence(mm):
     check_forward(mm, [1500, 700], 4, 1, 128)
     check_backward(mm, [1500, 700], 4, 1, 128)
