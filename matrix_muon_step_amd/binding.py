@@ -354,24 +354,35 @@ def _torch_stream(stream, device=None):
     return stream
 
 
-@contextlib.contextmanager
-def _on(device, stream):
+class _on:
     """Runs a call with `device` current and its stream entered (so that
-    allocations made for the call belong to that stream); yields the stream."""
-    import torch
+    allocations made for the call belong to that stream); yields the stream.
+    Where both are current already there is nothing to enter."""
 
-    if stream is None and (device is None or device.index == torch.cuda.current_device()):
-        yield torch.cuda.current_stream()  # already current: nothing to enter
-        return
-    if device is None:
-        st = _torch_stream(stream)
-        with torch.cuda.stream(st):
-            yield st
-        return
-    with torch.cuda.device(device):
+    __slots__ = ("_device", "_stream", "_stack")
+
+    def __init__(self, device, stream):
+        self._device = device
+        self._stream = stream
+        self._stack = None
+
+    def __enter__(self):
+        import torch
+
+        device, stream = self._device, self._stream
+        if stream is None and (device is None or device.index == torch.cuda.current_device()):
+            return torch.cuda.current_stream()
+        self._stack = contextlib.ExitStack()
+        if device is not None:
+            self._stack.enter_context(torch.cuda.device(device))
         st = _torch_stream(stream, device)
-        with torch.cuda.stream(st):
-            yield st
+        self._stack.enter_context(torch.cuda.stream(st))
+        return st
+
+    def __exit__(self, *exc):
+        if self._stack is not None:
+            return self._stack.__exit__(*exc)
+        return False
 
 
 def _alloc_workspace(nbytes: int, device):
@@ -860,6 +871,12 @@ class MuonCheckpoint:
         self.data = data
         self.tokens = int(tokens)
         self.cols = int(cols)
+        self._need = 0  # bytes, once asked for
+
+    def _bytes(self):
+        if not self._need:
+            self._need = muon_checkpoint_bytes(self.tokens, self.cols)
+        return self._need
 
 
 def muon_checkpoint_bytes(tokens: int, cols: int) -> int:
@@ -907,7 +924,7 @@ def _checkpoint_data(c, what):
 
     if not c.data.is_cuda or c.data.dtype != torch.uint8 or not c.data.is_contiguous():
         raise ValueError(f"{what}: the checkpoint's data must be a contiguous uint8 GPU tensor")
-    if c.data.numel() < muon_checkpoint_bytes(c.tokens, c.cols):
+    if c.data.numel() < c._bytes():
         raise ValueError(f"{what}: the checkpoint's data is too small")
 
 

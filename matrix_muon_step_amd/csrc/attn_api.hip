@@ -92,14 +92,16 @@ muon_status_t check_tensors(const std::vector<Tensor>& ts, int64_t tokens, int64
   if (tokens == 0) return MUON_OK;  // nothing is read or written
   for (const Tensor& t : ts) {
     const muon_heads_t& v = *t.v;
-    const std::string id = std::string("muon: attention tensor ") + t.name;
-    if (!v.data) return fail(MUON_ERR_INVALID_ARG, id + " is NULL");
-    if (v.token_stride < 0 || v.head_stride < 0) return fail(MUON_ERR_INVALID_ARG, id + " has a negative stride");
+    auto refuse = [&](muon_status_t st, const char* why) {
+      return fail(st, std::string("muon: attention tensor ") + t.name + why);
+    };
+    if (!v.data) return refuse(MUON_ERR_INVALID_ARG, " is NULL");
+    if (v.token_stride < 0 || v.head_stride < 0) return refuse(MUON_ERR_INVALID_ARG, " has a negative stride");
     if ((reinterpret_cast<uintptr_t>(v.data) & 15u) || v.token_stride % 8 != 0 || v.head_stride % 8 != 0)
-      return fail(MUON_ERR_ALIGN, id + ": data must be 16-byte aligned and strides multiples of 8");
+      return refuse(MUON_ERR_ALIGN, ": data must be 16-byte aligned and strides multiples of 8");
     if (v.token_stride > MUON_MAX_TOKEN_STRIDE)
-      return fail(MUON_ERR_UNSUPPORTED, id + ": token_stride exceeds MUON_MAX_TOKEN_STRIDE");
-    if (v.head_stride > (int64_t{1} << 48)) return fail(MUON_ERR_UNSUPPORTED, id + ": head_stride too large");
+      return refuse(MUON_ERR_UNSUPPORTED, ": token_stride exceeds MUON_MAX_TOKEN_STRIDE");
+    if (v.head_stride > (int64_t{1} << 48)) return refuse(MUON_ERR_UNSUPPORTED, ": head_stride too large");
   }
   for (const Tensor& t : ts) {
     if (!t.writable) continue;
