@@ -446,7 +446,8 @@ muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_pa
  * muon_checkpoint_write fills every item's data from its x;
  * muon_checkpoint_read writes the held values to x (each exact in bfloat16),
  * for backward passes that need the input itself.  One launch per 32 items;
- * buffers that a call writes overlap nothing else of the call. */
+ * buffers that a call writes overlap nothing else of the call (a strided x
+ * counts from its first to its last element). */
 typedef struct muon_checkpoint {
   void* x;
   int64_t x_stride;

@@ -372,11 +372,12 @@ class _on:
         device, stream = self._device, self._stream
         if stream is None and (device is None or device.index == torch.cuda.current_device()):
             return torch.cuda.current_stream()
-        self._stack = contextlib.ExitStack()
-        if device is not None:
-            self._stack.enter_context(torch.cuda.device(device))
-        st = _torch_stream(stream, device)
-        self._stack.enter_context(torch.cuda.stream(st))
+        with contextlib.ExitStack() as stack:  # undone if something here raises
+            if device is not None:
+                stack.enter_context(torch.cuda.device(device))
+            st = _torch_stream(stream, device)
+            stack.enter_context(torch.cuda.stream(st))
+            self._stack = stack.pop_all()
         return st
 
     def __exit__(self, *exc):

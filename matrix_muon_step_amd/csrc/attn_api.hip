@@ -20,6 +20,7 @@ struct muon_packing_s {
   const AttnTile* by_query;
   const AttnTile* by_key;
   uintptr_t lo, hi;  // the table's bytes
+  int64_t longest;   // tokens of the longest sequence
 };
 
 namespace {
@@ -227,6 +228,7 @@ muon_status_t muon_packing_create(const int64_t* lengths, int64_t n, void* table
     p->by_key = p->by_query + tiles;
     p->lo = reinterpret_cast<uintptr_t>(table);
     p->hi = p->lo + need;
+    p->longest = n > 0 ? *std::max_element(lengths, lengths + n) : 0;
     *out = p.release();
     return MUON_OK;
   });
@@ -279,6 +281,7 @@ muon_status_t muon_attention(const muon_attention_t* args, muon_packing_t packin
     a.by_query = packing->by_query;
     a.by_key = packing->by_key;
     a.n_tiles = static_cast<int32_t>(packing->n_tiles);
+    a.longest = static_cast<int32_t>(packing->longest);
     const hipError_t e = launch_attention(a, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? MUON_OK : hip_fail(e, "attention launch");
   });
@@ -342,6 +345,7 @@ muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_pa
     a.by_query = packing->by_query;
     a.by_key = packing->by_key;
     a.n_tiles = static_cast<int32_t>(packing->n_tiles);
+    a.longest = static_cast<int32_t>(packing->longest);
     const hipError_t e = launch_attention_backward(a, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? MUON_OK : hip_fail(e, "attention backward launch");
   });

@@ -44,6 +44,7 @@ struct AttnArgs {
   const AttnTile* by_query;    // tiles, most keys first
   const AttnTile* by_key;      // tiles, most queries first
   int32_t n_tiles;
+  int32_t longest;             // tokens of the longest sequence
 };
 
 hipError_t launch_attention(const AttnArgs& a, hipStream_t s);

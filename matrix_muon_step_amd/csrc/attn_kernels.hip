@@ -255,46 +255,92 @@ __device__ __forceinline__ void atomic_max_float(float* p, float x) {
   else atomicMin(reinterpret_cast<unsigned int*>(p), static_cast<unsigned int>(b));
 }
 
+// Work-groups of the kernels that own query rows (forward, dQ): 128 query rows
+// of one head; key and value tiles of 64 rows stream through a double buffer
+// in LDS.  4 waves of 32 rows, or (SPLIT = 2) 8 of them, wave w and w + 4 with
+// the same rows and every other key tile, joined at the end: half the turns
+// for the longest rows (see split_keys).
+template <int DP, bool EXACT, int SPLIT>
+struct KeyStream {
+  using G = Geo<DP>;
+  static constexpr int TURN = SPLIT * 2 * G::TILEB;  // bytes of a turn's tiles
+  TileLoad<DP, EXACT, 4> kl, vl;
+  int64_t kstep, vstep;
+  int rows;    // what the sequence has from the next tile's first row on
+  int fill;    // place of the next tile in LDS
+  __device__ __forceinline__ KeyStream(const AttnArgs& a, const AttnTile& t, int kv, int wave, int lane)
+      : kl(a.k, t.row0 + static_cast<int64_t>(wave >> 2) * kAttnStep, kv, a.head_dim, wave & 3, lane),
+        vl(a.v, t.row0 + static_cast<int64_t>(wave >> 2) * kAttnStep, kv, a.head_dim, wave & 3, lane) {
+    kstep = static_cast<int64_t>(kl.ts2) * (SPLIT * kAttnStep);
+    vstep = static_cast<int64_t>(vl.ts2) * (SPLIT * kAttnStep);
+    rows = t.len - (wave >> 2) * kAttnStep;
+    fill = (wave >> 2) * 2 * G::TILEB;
+  }
+  // Starts the loads of this wave's share of the next turn's tiles.
+  __device__ __forceinline__ void next(LAS unsigned char* lds, int wave) {
+    kl.load(rows, lds + fill, wave & 3);
+    vl.load(rows, lds + fill + G::TILEB, wave & 3);
+    kl.move(kstep);
+    vl.move(vstep);
+    rows -= SPLIT * kAttnStep;
+    fill ^= TURN;
+  }
+};
+
+// Hands a wave's accumulators over through LDS, 1 KB per four registers.
+template <int DP>
+__device__ __forceinline__ void put_acc(LAS unsigned char* __restrict__ p, const f32x16_t (&acc)[Geo<DP>::DB]) {
+#pragma unroll
+  for (int i = 0; i < Geo<DP>::DB * 4; ++i) {
+    const f32x16_t& x = acc[i >> 2];
+    const int g = 4 * (i & 3);
+    *(LAS f32x4_t*)(p + i * 1024) = (f32x4_t){x[g], x[g + 1], x[g + 2], x[g + 3]};
+  }
+}
+// acc = acc * mine + theirs * other
+template <int DP>
+__device__ __forceinline__ void join_acc(const LAS unsigned char* __restrict__ p, f32x16_t (&acc)[Geo<DP>::DB], float mine,
+                                         float other) {
+#pragma unroll
+  for (int i = 0; i < Geo<DP>::DB * 4; ++i) {
+    const f32x4_t o = *(const LAS f32x4_t*)(p + i * 1024);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[i >> 2][4 * (i & 3) + k] = fmaf(o[k], other, acc[i >> 2][4 * (i & 3) + k] * mine);
+  }
+}
+
 // ------------------------------------------------------------------ forward
-// One work-group: 128 query rows of one head, 4 waves of 32 rows; key and
-// value tiles of 64 rows stream through a double buffer in LDS.  A wave reads
-// every fragment of a tile for its 32 rows, so with heads of 128 the LDS (128
-// bytes a cycle) is as busy as the matrix cores; 32 rows leave room for two
-// work-groups to a unit (four with heads of 64), whose waves share a SIMD
-// without a common barrier: one's exponentials run under the other's products.
+// A wave reads every fragment of a tile for its 32 rows, so with heads of 128
+// the LDS (128 bytes a cycle) is as busy as the matrix cores; 32 rows leave
+// room for two work-groups to a unit (four with heads of 64), whose waves
+// share a SIMD without a common barrier: one's exponentials run under the
+// other's products.
 // 8192 tokens, 32 heads of 128 over 8 key heads: 527 us, 1.04 PFLOP/s, the
 // matrix cores 54% busy at the 1.9 GHz that the card holds under this load.
 // 4100 tokens in ten sequences, 25 heads of 64: 27 us; the longest sequence's
 // 21 turns (about 1 us each) bound it.
-template <int DP, bool EXACT>
-__global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attention_kernel(const AttnArgs a) {
+template <int DP, bool EXACT, int SPLIT>
+__global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kernel(const AttnArgs a) {
   using G = Geo<DP>;
-  __shared__ __align__(1024) unsigned char smem[4 * G::TILEB];
+  using KS = KeyStream<DP, EXACT, SPLIT>;
+  static_assert(SPLIT == 1 || 2 * KS::TURN >= 4 * (G::DB * 4096 + 1024), "the join fits the buffer");
+  __shared__ __align__(1024) unsigned char smem[2 * KS::TURN];
   LAS unsigned char* lds = (LAS unsigned char*)smem;
   const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = wave >> 2;
   const int hx = blockIdx.x % a.heads;
   const AttnTile t = a.by_query[blockIdx.x / a.heads];
   const int kv = hx % a.kv_heads;
   const int head = kv * (a.heads / a.kv_heads) + hx / a.kv_heads;
-  const int nk = (min(t.len, t.first + kAttnRows) + kAttnStep - 1) / kAttnStep;
-  const int wq0 = t.first + 32 * wave;   // the wave's first query row in its sequence
+  const int turns = (min(t.len, t.first + kAttnRows) + SPLIT * kAttnStep - 1) / (SPLIT * kAttnStep);
+  const int wq0 = t.first + 32 * (wave & 3);   // the wave's first query row in its sequence
   const int q = wq0 + (lane & 31);
   const float c = a.scale * kLog2e;
   const float slack = kSlackLog2 / c;
 
-  TileLoad<DP, EXACT, 4> kl(a.k, t.row0, kv, a.head_dim, wave, lane), vl(a.v, t.row0, kv, a.head_dim, wave, lane);
+  KS stream(a, t, kv, wave, lane);
   const FragOff fo = frag_offsets(lane);
-  int fill = 0, fill_row = 0;  // the buffer (byte offset) and first key of the next tile to load
-  auto issue = [&]() {
-    kl.load(t.len - fill_row, lds + fill, wave);
-    vl.load(t.len - fill_row, lds + fill + G::TILEB, wave);
-    kl.move(static_cast<int64_t>(kl.ts2) * kAttnStep);
-    vl.move(static_cast<int64_t>(vl.ts2) * kAttnStep);
-    fill_row += kAttnStep;
-    fill ^= 2 * G::TILEB;
-  };
-  issue();
+  stream.next(lds, wave);
   bf16x8_t qf[G::KS];
   own_rows<DP>(a.q.p + ((static_cast<int64_t>(t.row0) + wq0) * a.q.ts + head * a.q.hs) * 2, a.q.ts, a.head_dim, t.len - wq0,
                lane, qf);
@@ -303,10 +349,10 @@ __global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attention_kernel(const 
 #pragma unroll
   for (int db = 0; db < G::DB; ++db) o[db] = (f32x16_t)(0.f);
   float m_top = -kInf, m_ref = -kInf, l = 0.f;  // l: this lane's half of the keys
-  for (int kt = 0; kt < nk; ++kt) {
-    const int k0 = kt * kAttnStep, cur = fill ^ (2 * G::TILEB);
+  for (int it = 0; it < turns; ++it) {
+    const int k0 = (it * SPLIT + part) * kAttnStep, cur = stream.fill ^ KS::TURN;
     next_tile();
-    if (kt + 1 < nk) issue();
+    if (it + 1 < turns) stream.next(lds, wave);
     if (k0 > wq0 + 31 || wq0 >= t.len) continue;  // every key lies behind the wave's rows, or it has none
     const LAS unsigned char* kt_lds = lds + cur;
     const LAS unsigned char* vt_lds = kt_lds + G::TILEB;
@@ -354,13 +400,32 @@ __global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attention_kernel(const 
       for (int db = 0; db < G::DB; ++db) o[db] = mfma(col_frag<DP>(vt_lds, fo, db, t16), p, o[db]);
     }
   }
-  const bool live = q < t.len;
   l = half_sum(l);
-  store_rows<DP>(a.o, static_cast<int64_t>(t.row0) + q, head, a.head_dim, live, lane, o, 1.f / l);
-  if (live && h == 0) {
-    const float ref = m_ref == -kInf ? 0.f : m_ref * c;  // as the exponentials had it
-    gst(a.lse + head * a.lse_stride + t.row0 + q, (ref + __builtin_amdgcn_logf(l)) * kLn2);
+  float ref = m_ref == -kInf ? 0.f : m_ref * c;  // as the exponentials had it
+  if constexpr (SPLIT == 2) {
+    // The second half's sums, reference and largest logit, brought to a
+    // common reference.
+    LAS unsigned char* at = lds + (wave & 3) * (G::DB * 4096 + 1024) + lane * 16;
+    next_tile();
+    if (part == 1) {
+      put_acc<DP>(at, o);
+      *(LAS f32x4_t*)(at + G::DB * 4096) = (f32x4_t){m_ref, m_top, l, 0.f};
+    }
+    next_tile();
+    if (part == 1) return;
+    const f32x4_t x = *(const LAS f32x4_t*)(at + G::DB * 4096);
+    const float m = fmaxf(m_ref, x[0]), common = m == -kInf ? 0.f : m * c;
+    // without a reference the sums are zero (or NaN): as they are
+    const float mine = m_ref == -kInf ? 1.f : __builtin_amdgcn_exp2f(ref - common);
+    const float other = x[0] == -kInf ? 1.f : __builtin_amdgcn_exp2f(x[0] * c - common);
+    join_acc<DP>(at, o, mine, other);
+    l = fmaf(x[2], other, l * mine);
+    m_top = fmaxf(m_top, x[1]);
+    ref = common;
   }
+  const bool live = q < t.len;
+  store_rows<DP>(a.o, static_cast<int64_t>(t.row0) + q, head, a.head_dim, live, lane, o, 1.f / l);
+  if (live && h == 0) gst(a.lse + head * a.lse_stride + t.row0 + q, (ref + __builtin_amdgcn_logf(l)) * kLn2);
   if (a.max_logit) {
     // A row whose sum is NaN has an infinite logit, or else a NaN.
     float top = !live ? -kInf : l != l && m_top < kInf ? __builtin_nanf("") : m_top * a.scale;
@@ -374,44 +439,34 @@ __global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attention_kernel(const 
 }
 
 // ------------------------------------------------------------ backward: dQ
-// One work-group: 128 query rows of one head, 4 waves of 32 rows; key and
-// value tiles stream past, as in the forward pass and bound by the same.  Also
-// forms delta and leaves it, with lse in base 2, for the dK/dV kernel that
+// As in the forward pass, and bound by the same.  Also forms delta and leaves it, with lse in base 2, for the dK/dV kernel that
 // follows.  Scores and their gradients are formed again here rather than
 // passed on: dQ summed by atomics from the dK/dV kernel would save 2 of the 7
 // products of the two kernels, but with an order that changes from run to
 // run.  8192 tokens, 32 heads of 128: 690 us, 1.19 PFLOP/s, matrix cores 57%
 // busy (with one wave a SIMD, 1240 us).
-template <int DP, bool EXACT>
-__global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attention_dq_kernel(const AttnArgs a) {
+template <int DP, bool EXACT, int SPLIT>
+__global__ __launch_bounds__(256 * SPLIT, DP == 64 && SPLIT == 1 ? 4 : 2) void attention_dq_kernel(const AttnArgs a) {
   using G = Geo<DP>;
-  __shared__ __align__(1024) unsigned char smem[4 * G::TILEB];
+  using KS = KeyStream<DP, EXACT, SPLIT>;
+  __shared__ __align__(1024) unsigned char smem[2 * KS::TURN];
   LAS unsigned char* lds = (LAS unsigned char*)smem;
   const int lane = threadIdx.x & 63, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = wave >> 2;
   const int hx = blockIdx.x % a.heads;
   const AttnTile t = a.by_query[blockIdx.x / a.heads];
   const int kv = hx % a.kv_heads;
   const int head = kv * (a.heads / a.kv_heads) + hx / a.kv_heads;
-  const int nk = (min(t.len, t.first + kAttnRows) + kAttnStep - 1) / kAttnStep;
-  const int wq0 = t.first + 32 * wave;
+  const int turns = (min(t.len, t.first + kAttnRows) + SPLIT * kAttnStep - 1) / (SPLIT * kAttnStep);
+  const int wq0 = t.first + 32 * (wave & 3);
   const int q = wq0 + (lane & 31);
   const bool live = q < t.len;
   const int64_t row = static_cast<int64_t>(t.row0) + q;
   const float c = a.scale * kLog2e;
 
-  TileLoad<DP, EXACT, 4> kl(a.k, t.row0, kv, a.head_dim, wave, lane), vl(a.v, t.row0, kv, a.head_dim, wave, lane);
+  KS stream(a, t, kv, wave, lane);
   const FragOff fo = frag_offsets(lane);
-  int fill = 0, fill_row = 0;  // the buffer (byte offset) and first key of the next tile to load
-  auto issue = [&]() {
-    kl.load(t.len - fill_row, lds + fill, wave);
-    vl.load(t.len - fill_row, lds + fill + G::TILEB, wave);
-    kl.move(static_cast<int64_t>(kl.ts2) * kAttnStep);
-    vl.move(static_cast<int64_t>(vl.ts2) * kAttnStep);
-    fill_row += kAttnStep;
-    fill ^= 2 * G::TILEB;
-  };
-  issue();
+  stream.next(lds, wave);
   const int64_t row0 = static_cast<int64_t>(t.row0) + wq0;
   bf16x8_t qf[G::KS], gf[G::KS];
   own_rows<DP>(a.q.p + (row0 * a.q.ts + head * a.q.hs) * 2, a.q.ts, a.head_dim, t.len - wq0, lane, qf);
@@ -427,7 +482,7 @@ __global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attention_dq_kernel(con
     delta = half_sum(delta);
   }
   const float lse2 = live ? gld<float>(a.lse + head * a.lse_stride + row) * kLog2e : 0.f;
-  if (live && h == 0) {
+  if (live && h == 0 && part == 0) {
     gst(a.row_lse2 + head * a.row_stride + row, lse2);
     gst(a.row_delta + head * a.row_stride + row, delta);
   }
@@ -435,10 +490,10 @@ __global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attention_dq_kernel(con
   f32x16_t dq[G::DB];
 #pragma unroll
   for (int db = 0; db < G::DB; ++db) dq[db] = (f32x16_t)(0.f);
-  for (int kt = 0; kt < nk; ++kt) {
-    const int k0 = kt * kAttnStep, cur = fill ^ (2 * G::TILEB);
+  for (int it = 0; it < turns; ++it) {
+    const int k0 = (it * SPLIT + part) * kAttnStep, cur = stream.fill ^ KS::TURN;
     next_tile();
-    if (kt + 1 < nk) issue();
+    if (it + 1 < turns) stream.next(lds, wave);
     if (k0 > wq0 + 31 || wq0 >= t.len) continue;
     const LAS unsigned char* kt_lds = lds + cur;
     const LAS unsigned char* vt_lds = kt_lds + G::TILEB;
@@ -463,6 +518,14 @@ __global__ __launch_bounds__(256, DP == 64 ? 4 : 2) void attention_dq_kernel(con
         for (int db = 0; db < G::DB; ++db) dq[db] = mfma(col_frag<DP>(kt_lds, fo, db, 2 * b + s16), ds, dq[db]);
       }
     }
+  }
+  if constexpr (SPLIT == 2) {
+    LAS unsigned char* at = lds + (wave & 3) * (G::DB * 4096) + lane * 16;
+    next_tile();
+    if (part == 1) put_acc<DP>(at, dq);
+    next_tile();
+    if (part == 1) return;
+    join_acc<DP>(at, dq, 1.f, 1.f);
   }
   store_rows<DP>(a.dq, row, head, a.head_dim, live, lane, dq, a.scale);
 }
@@ -740,15 +803,29 @@ __global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a)
 
 namespace {
 
+// Whether rows are split over two wave groups: with up to two work-groups of
+// either kind to a unit, the longest sequence's turns are the call's time and
+// half of them pay for the join; shorter sequences and fuller cards lose by
+// it.  Forward / whole backward pass in us, whole | split: 4096 tokens, 12
+// heads of 64 (384 work-groups) 56 / 155 | 46 / 132, 16 of 128 (512) 92 / 272
+// | 85 / 269; 1290 tokens, 25 of 64 (275) 20.8 / 59 | 19.3 / 55; 4 x 1024
+// tokens, 16 of 128 (512) 30 / 94 | 34 / 102; 4096 tokens, 25 of 64 (800)
+// 75 / 241 | 72 / 251.
+bool split_keys(const AttnArgs& a) { return int64_t{a.n_tiles} * a.heads <= 512 && a.longest > 1024; }
+
 template <int DP, bool EXACT>
 hipError_t forward(const AttnArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((attention_kernel<DP, EXACT>), dim3(static_cast<uint32_t>(a.n_tiles) * a.heads), dim3(256), 0, s, a);
+  const dim3 grid(static_cast<uint32_t>(a.n_tiles) * a.heads);
+  if (split_keys(a)) hipLaunchKernelGGL((attention_kernel<DP, EXACT, 2>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((attention_kernel<DP, EXACT, 1>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <int DP, bool EXACT>
 hipError_t backward(const AttnArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((attention_dq_kernel<DP, EXACT>), dim3(static_cast<uint32_t>(a.n_tiles) * a.heads), dim3(256), 0, s, a);
+  const dim3 rows(static_cast<uint32_t>(a.n_tiles) * a.heads);
+  if (split_keys(a)) hipLaunchKernelGGL((attention_dq_kernel<DP, EXACT, 2>), rows, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((attention_dq_kernel<DP, EXACT, 1>), rows, dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 grid(static_cast<uint32_t>(a.n_tiles) * a.kv_heads);

@@ -116,7 +116,7 @@ GradPlan plan_grad(const muon_checkpoint_grad_t* mats, int64_t n) {
   for (int64_t i = 0; i < n; ++i) {
     const int64_t steps = tiles(mats[i].tokens, kCkTile);
     longest = std::max(longest, steps);
-    empty = empty || steps == 0;
+    empty = empty || (steps == 0 && !mats[i].accumulate);
     for (int c = 0; c < kNumGradCfg; ++c) {
       const int64_t t = tiles(mats[i].outs, kGradTile[c]) * tiles(mats[i].cols, kGradTile[c]);
       tiles_of[c] += t;

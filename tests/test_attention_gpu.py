@@ -125,6 +125,14 @@ def test_many_tiles(mm):
     check_backward(mm, lengths, 16, 8, 40)
 
 
+@pytest.mark.parametrize("lengths", [[1025], [1100, 3, 64], [1151, 0, 1], [2000]], ids=str)
+@pytest.mark.parametrize("heads,kv_heads,dim", [(3, 3, 64), (4, 2, 128), (2, 1, 40), (2, 2, 104)])
+def test_split_keys(mm, lengths, heads, kv_heads, dim):
+    """Few rows of long sequences: their keys are split over two wave groups."""
+    check_forward(mm, lengths, heads, kv_heads, dim, behind=1, sharp=4.0)
+    check_backward(mm, lengths, heads, kv_heads, dim, behind=1)
+
+
 def test_long_sequence(mm):
     check_forward(mm, [1500, 700], 4, 1, 128)
     check_backward(mm, [1500, 700], 4, 1, 128)

@@ -20,12 +20,12 @@ def lengths(*n):
 class packing_s(ctypes.Structure):
     _fields_ = [("device", ctypes.c_int), ("tokens", ctypes.c_int64), ("n_tiles", ctypes.c_int64),
                 ("by_query", ctypes.c_void_p), ("by_key", ctypes.c_void_p), ("lo", ctypes.c_size_t),
-                ("hi", ctypes.c_size_t)]
+                ("hi", ctypes.c_size_t), ("longest", ctypes.c_int64)]
 
 
 def packing(tokens=100, tiles=1):
     # of a device that is not there: what passes every check ends at that one
-    return packing_s(77, tokens, tiles, BASE, BASE + 64, BASE, BASE + 4096)
+    return packing_s(77, tokens, tiles, BASE, BASE + 64, BASE, BASE + 4096, tokens)
 
 
 # ---------------------------------------------------------------- packings
