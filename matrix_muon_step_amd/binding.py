@@ -354,6 +354,27 @@ def _torch_stream(stream, device=None):
     return stream
 
 
+class _current:
+    """The current stream of the current device, by its handle: a torch stream
+    object costs 2.5 us to make, more than the rest of a call's bookkeeping."""
+
+    __slots__ = ("cuda_stream",)
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+    @property
+    def device(self):
+        import torch
+
+        return torch.device("cuda", torch.cuda.current_device())
+
+    def torch_stream(self):
+        import torch
+
+        return torch.cuda.current_stream()
+
+
 class _on:
     """Runs a call with `device` current and its stream entered (so that
     allocations made for the call belong to that stream); yields the stream.
@@ -370,8 +391,10 @@ class _on:
         import torch
 
         device, stream = self._device, self._stream
-        if stream is None and (device is None or device.index == torch.cuda.current_device()):
-            return torch.cuda.current_stream()
+        if stream is None:
+            index = torch.cuda.current_device()
+            if device is None or device.index == index:
+                return _current(torch._C._cuda_getCurrentRawStream(index))
         with contextlib.ExitStack() as stack:  # undone if something here raises
             if device is not None:
                 stack.enter_context(torch.cuda.device(device))
@@ -699,7 +722,7 @@ class MuonPacking:
         if device is not None and device != self.device:
             raise ValueError(f"the packing is on {self.device}, the call's tensors on {device}")
         if stream.cuda_stream != self._stream:
-            self._table.record_stream(stream)
+            self._table.record_stream(stream.torch_stream() if isinstance(stream, _current) else stream)
         return ctypes.c_void_p(self._h)
 
     def close(self) -> None:
