@@ -604,6 +604,18 @@ __device__ __forceinline__ void write_msg(LAS unsigned char* __restrict__ p, con
   *(LAS bf16x8_t*)(p + 1024) = x[1];
 }
 
+// The lane number, computed where it is written (two instructions) instead of
+// kept in a register: a kernel without one to spare would reload what depends
+// on it from scratch memory, and wait there for the tile loads under way too
+// (4100 tokens, 25 heads of 64: dK/dV 53 us, 44 without that).
+__device__ __forceinline__ int fresh_lane() {
+  int l = 0;
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+#endif
+  return l;
+}
+
 // The tiles that stream past a key tile: from the sequence's last rows back to
 // the diagonal, every query head of the group in turn, so that work-groups of
 // one key head read the same tiles at about the same time.
@@ -633,12 +645,12 @@ struct QueryStream {
   }
   // Starts this wave's loads of the next of RING tiles.
   template <int RING>
-  __device__ __forceinline__ void next(int len, LAS unsigned char* lds, int wave, int lane) {
+  __device__ __forceinline__ void next(int len, LAS unsigned char* lds, int wave) {
     LAS unsigned char* dst = lds + fill;
     ql.load(len - row, dst, wave);
     gl.load(len - row, dst + Geo<DP>::TILEB, wave);
     if (wave < 2)
-      load_lds<true, 0>(reinterpret_cast<const unsigned char*>(stat), 4u * min(len - row, kAttnStep), lane * 4,
+      load_lds<true, 0>(reinterpret_cast<const unsigned char*>(stat), 4u * min(len - row, kAttnStep), fresh_lane() * 4,
                         dst + L::ROWS + wave * kAttnStep * 4);
     fill = fill == (RING - 1) * L::STAGE ? 0 : fill + L::STAGE;
     if (++head == group) {
@@ -705,16 +717,16 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
     const bf16x8_t other[2] = {half == 0 ? ds[0] : p[0], half == 0 ? ds[1] : p[1]};
     write_msg(lds + out + turn, other);
   };
-  stream.template next<3>(t.len, lds, wave, lane);
+  stream.template next<3>(t.len, lds, wave);
   next_tile();
-  if (total > 1) stream.template next<3>(t.len, lds, wave, lane);
+  if (total > 1) stream.template next<3>(t.len, lds, wave);
   dkv_scores<DP>(lds + cur, fo, half, kf, vf, s, dp);
   mask();
   dkv_softmax<DP>(lds + cur, half, h, c, s, dp);
   pass_on();
   for (int it = 1; it < total; ++it) {
     next_tile();  // tile `it` and the messages of turn it - 1 are there, tile it - 2 is done with
-    if (it + 1 < total) stream.template next<3>(t.len, lds, wave, lane);
+    if (it + 1 < total) stream.template next<3>(t.len, lds, wave);
     const int prev = cur + sum_of;
     cur = cur == 2 * L::STAGE ? 0 : cur + L::STAGE;
     turn ^= 8 * 2048;
@@ -761,7 +773,7 @@ __global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a)
   const FragOff fo = frag_offsets(lane);
   QueryStream<DP, EXACT, 4> stream(a, t, kv, nq, wave, lane);
   int q0 = stream.row, head = 0, cur = 0;
-  stream.template next<2>(t.len, lds, wave, lane);
+  stream.template next<2>(t.len, lds, wave);
   const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
   bf16x8_t kf[G::KS], vf[G::KS];
   own_rows<DP>(a.k.p + (krow0 * a.k.ts + kv * a.k.hs) * 2, a.k.ts, a.head_dim, t.len - wk0, lane, kf);
@@ -771,7 +783,7 @@ __global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a)
   for (int db = 0; db < G::DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
   for (int it = 0; it < total; ++it) {
     next_tile();
-    if (it + 1 < total) stream.template next<2>(t.len, lds, wave, lane);
+    if (it + 1 < total) stream.template next<2>(t.len, lds, wave);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int qs = q0 + 32 * b;
