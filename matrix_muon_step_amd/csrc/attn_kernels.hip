@@ -844,8 +844,10 @@ hipError_t backward(const AttnArgs& a, hipStream_t s) {
   // Up to two key tiles for each of the 256 compute units, the longest one's
   // turns are what takes the time, and the pair kernel's are half as long;
   // with more the three-to-a-unit kernel wins.  dQ, dK and dV with heads of 64,
-  // us, pair | three: 1290 tokens, 25 heads (275 tiles) 58 | 71; 8 x 512
-  // (800) 70 | 51; 4096 (800) 272 | 253; 64 x 64 (1600) 52 | 37.
+  // us, pair | three: 1290 tokens, 25 heads (275 tiles) 53 | 60; 4096 tokens,
+  // 12 heads (384) 131 | 159; 8 x 512, 16 heads (512) 41 | 37; 25 heads: 2500
+  // (500) 116 | 119, 8 x 512 (800) 70 | 50, 4096 (800) 272 | 228, 64 x 64
+  // (1600) 52 | 37.
   if (DP == 64 && grid.x > 512) hipLaunchKernelGGL((attention_dkv_kernel<64, EXACT>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((attention_dkv_pair_kernel<DP, EXACT>), grid, dim3(512), 0, s, a);
   return hipGetLastError();
