@@ -349,8 +349,8 @@ __device__ __forceinline__ void grad_tile(const GradDesc& d, int m0, int n0, int
   // (the last block again past the last column: those columns of G are not stored)
   ld.xp = d.codes + (static_cast<int64_t>(s0) * d.blocks + min(n0 / kCkTile + wave, d.blocks - 1)) * kCkBlockBytes;
   ld.left = d.tokens - s0 * 32;
-  // whole 16-byte chunks: what the last one holds past `outs` meets only rows
-  // of G that are not stored
+  // whole 16-byte chunks (aligned: none crosses a page): what the last one holds
+  // past `outs` meets only rows of G that are not stored
   ld.tail = (width * 2 + 15) / 16 * 16;
 #pragma unroll
   for (int i = 0; i < C::PA; ++i) ld.off[i] = static_cast<uint32_t>((k0 + i * C::ROWS) * ld.ld2 + ch * 16);
@@ -362,9 +362,10 @@ __device__ __forceinline__ void grad_tile(const GradDesc& d, int m0, int n0, int
       const int k = k0 + i * C::ROWS;
       held[i] = (uint4){0, 0, 0, 0};
       if (k < ld.left && ch * 8 < width) {
-        // only the last row of dY may not be read past its end
+        // A chunk may run on into the rows behind (of narrow matrices, into
+        // several), not past dY's last element.
         const unsigned char* p = ld.ap + static_cast<int64_t>(k) * ld.ld2;
-        if (k + 1 < ld.left || ch * 8 + 8 <= d.outs - m0) held[i] = gld<uint4>(p + ch * 16);
+        if (min(ld.left - 1 - k, 8) * (ld.ld2 >> 1) + d.outs - m0 >= ch * 8 + 8) held[i] = gld<uint4>(p + ch * 16);
         else held[i] = load_row16<2>(p, ch * 8, d.outs - m0);
       }
     }

@@ -157,6 +157,22 @@ def test_grad(mm, tokens, outs, cols, pad, g_type):
     check_grad(dy, xh, G, old)
 
 
+@pytest.mark.parametrize("outs", range(1, 9))
+@pytest.mark.parametrize("tokens", [2, 33, 300])
+def test_grad_of_narrow_rows(mm, tokens, outs):
+    """Rows of a few elements: a 16-byte read spans several of them, and near dY's end none may be one."""
+    print(f"[case] gradient {tokens} x {outs} x 40", flush=True)
+    x = activation(tokens, 40, BF16)
+    saved = mm.muon_checkpoint_write([x])[0]
+    xh = np64(mm.muon_checkpoint_read([saved], dtype=F32)[0])
+    room = torch.full((tokens * outs + 64,), math.nan, dtype=BF16, device="cuda")
+    dy = room[32:32 + tokens * outs].view(tokens, outs)  # NaN before the first element and behind the last
+    dy.copy_(upstream(tokens, outs, 0))
+    G = torch.empty((outs, 40), device="cuda")
+    mm.muon_checkpoint_grad([(dy, saved, G)])
+    check_grad(dy, xh, G)
+
+
 def test_grad_no_tokens(mm):
     saved = mm.muon_checkpoint_write([torch.empty((0, 40), dtype=BF16, device="cuda")])[0]
     G = torch.full((24, 40), 3.0, device="cuda")
