@@ -383,7 +383,9 @@ typedef struct muon_heads {
  *              (query projection with head_dim * heads / kv_heads rows per
  *              entry, key projection with head_dim).  A NaN logit gives
  *              NaN, +infinity where the row's largest logit is that.
- *   heads      a multiple of kv_heads >= 1, at most MUON_MAX_HEADS
+ *   heads      a multiple of kv_heads >= 1, at most MUON_MAX_HEADS; times the
+ *              128-row pieces of the packing's sequences (the last of each may
+ *              be shorter) below MUON_MAX_ATTENTION_ITEMS
  *   head_dim   a multiple of 8, 8..128 (others: MUON_ERR_UNSUPPORTED)
  *   scale      finite, > 0
  * Rows of o and lse behind the packing's last sequence are left as they
@@ -391,6 +393,7 @@ typedef struct muon_heads {
  * or infinity in a sequence reaches rows of that sequence only (there it
  * may reach rows before it too: 0 * NaN is NaN). */
 #define MUON_MAX_HEADS 4096
+#define MUON_MAX_ATTENTION_ITEMS 8388608
 typedef struct muon_attention {
   muon_heads_t q, k, v, o;
   float* lse;
@@ -442,7 +445,8 @@ muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_pa
  *   data      DEVICE, 256-byte aligned, muon_checkpoint_bytes(tokens, cols)
  *             bytes (cols and tokens rounded up to 32, plus 1 / 1024); an
  *             opaque layout, made for muon_checkpoint_grad
- *   tokens    >= 0, <= MUON_MAX_TOKENS; cols: 1 .. MUON_MAX_DIM
+ *   tokens    >= 0, <= MUON_MAX_TOKENS; cols: 1 .. MUON_MAX_DIM; to write and
+ *             read, ceil(tokens / 32) * ceil(cols / 256) < 2^24
  * muon_checkpoint_write fills every item's data from its x;
  * muon_checkpoint_read writes the held values to x (each exact in bfloat16),
  * for backward passes that need the input itself.  One launch per 32 items;

@@ -30,6 +30,9 @@ muon_status_t check_count(const void* items, int64_t n) {
   return MUON_OK;
 }
 
+// Work-groups of 256 lanes that a launch takes: fewer than 2^32 lanes.
+constexpr int64_t kMaxGroups = int64_t{1} << 24;
+
 muon_status_t move_all(const muon_checkpoint_t* items, int64_t n, bool write, void* stream) {
   muon_status_t st = check_count(items, n);
   if (st != MUON_OK) return st;
@@ -44,6 +47,8 @@ muon_status_t move_all(const muon_checkpoint_t* items, int64_t n, bool write, vo
     if (m.x_stride < m.cols) return fail(MUON_ERR_INVALID_ARG, id + ": x_stride is smaller than cols");
     if (m.x_stride > (int64_t{1} << 40)) return fail(MUON_ERR_UNSUPPORTED, id + ": x_stride too large");
     if (m.tokens == 0) continue;
+    if (tiles(m.tokens, kCkTile) * tiles(m.cols, kCkGroupCols) >= kMaxGroups)
+      return fail(MUON_ERR_UNSUPPORTED, id + " is too large for one launch");
     if (!m.x || !m.data) return fail(MUON_ERR_INVALID_ARG, id + " has a NULL x or data");
     const uintptr_t es = m.x_dtype == MUON_F32 ? 4 : 2;
     const uintptr_t x = reinterpret_cast<uintptr_t>(m.x), p = reinterpret_cast<uintptr_t>(m.data);
@@ -67,8 +72,7 @@ muon_status_t move_all(const muon_checkpoint_t* items, int64_t n, bool write, vo
     if (m.tokens == 0) continue;
     const int64_t nS = tiles(m.cols, kCkTile), groups = tiles(m.cols, kCkGroupCols);
     const int64_t work = tiles(m.tokens, kCkTile) * groups;
-    if (work > (int64_t{1} << 31) - 1) return fail(MUON_ERR_UNSUPPORTED, "muon: checkpoint too large for one launch");
-    if (b.n == kCkBatch || b.prefix[b.n] + work > (int64_t{1} << 31) - 1) {
+    if (b.n == kCkBatch || b.prefix[b.n] + work >= kMaxGroups) {
       st = flush();
       if (st != MUON_OK) return st;
     }

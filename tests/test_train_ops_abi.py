@@ -151,6 +151,15 @@ def test_attention_refuses_views(change, status):
         assert call_backward(g) == status, name
 
 
+@pytest.mark.parametrize("make,call", [(forward, call_forward), (backward, call_backward)], ids=["forward", "backward"])
+def test_attention_refuses_more_than_a_launch(make, call):
+    """Fewer than 2^32 lanes to a launch: 2^23 items of up to 512."""
+    assert call(make(), p=packing(tiles=1 << 21)) == mm.MUON_ERR_UNSUPPORTED    # 4 heads
+    # one fewer passes on to the device check
+    assert call(make(), p=packing(tiles=(1 << 21) - 1)) in (mm.MUON_ERR_HIP, mm.MUON_ERR_INVALID_ARG)
+    assert "items" not in mm.muon_last_error()
+
+
 def test_attention_null_arguments():
     L = mm.lib()
     assert L.muon_attention(None, ctypes.byref(packing()), None) == mm.MUON_ERR_INVALID_ARG
@@ -254,6 +263,9 @@ ITEMS = [
     (dict(x_dtype=5), mm.MUON_ERR_INVALID_ARG), (dict(x_stride=99), mm.MUON_ERR_INVALID_ARG),
     (dict(x=0), mm.MUON_ERR_INVALID_ARG), (dict(data=0), mm.MUON_ERR_INVALID_ARG), (dict(x=BASE * 2 + 1), mm.MUON_ERR_ALIGN),
     (dict(x=BASE * 2 + 2, x_dtype=mm.MUON_F32), mm.MUON_ERR_ALIGN), (dict(data=BASE * 3 + 128), mm.MUON_ERR_ALIGN),
+    # 2^24 work-groups of 256 lanes
+    (dict(tokens=1 << 29, cols=1, x_stride=1), mm.MUON_ERR_UNSUPPORTED),
+    (dict(tokens=1 << 21, cols=65536, x_stride=65536), mm.MUON_ERR_UNSUPPORTED),
     (dict(data=BASE * 2), mm.MUON_ERR_ALIAS), (dict(x=BASE * 3 + 512), mm.MUON_ERR_ALIAS),
 ]
 
