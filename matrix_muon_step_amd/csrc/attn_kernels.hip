@@ -311,14 +311,16 @@ __device__ __forceinline__ void join_acc(const LAS unsigned char* __restrict__ p
 
 // ------------------------------------------------------------------ forward
 // A wave reads every fragment of a tile for its 32 rows, so with heads of 128
-// the LDS (128 bytes a cycle) is as busy as the matrix cores; 32 rows leave
+// the LDS (at 128 bytes a cycle) works as long as the matrix cores; 32 rows leave
 // room for two work-groups to a unit (four with heads of 64), whose waves
 // share a SIMD without a common barrier: one's exponentials run under the
 // other's products.
-// 8192 tokens, 32 heads of 128 over 8 key heads: 527 us, 1.04 PFLOP/s, the
-// matrix cores 54% busy at the 1.9 GHz that the card holds under this load.
-// 4100 tokens in ten sequences, 25 heads of 64: 27 us; the longest sequence's
-// 21 turns (about 1 us each) bound it.
+// 8192 tokens, 32 heads of 128 over 8 key heads: 522 us, 1.05 PFLOP/s, the
+// matrix cores 55% busy at the 1.9 GHz that the card holds under this load.
+// 4100 tokens in ten sequences, 25 heads of 64: 27 us, the matrix cores 29%
+// busy (with heads of 64 the exponentials and what goes with them take about
+// twice the products' cycles); the longest sequence's 21 turns, about 1 us
+// each among the others', end last.
 template <int DP, bool EXACT, int SPLIT>
 __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kernel(const AttnArgs a) {
   using G = Geo<DP>;
@@ -439,11 +441,11 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
 }
 
 // ------------------------------------------------------------ backward: dQ
-// As in the forward pass, and bound by the same.  Also forms delta and leaves it, with lse in base 2, for the dK/dV kernel that
-// follows.  Scores and their gradients are formed again here rather than
+// As in the forward pass, and bound by the same.  Also forms delta and leaves
+// it, with lse in base 2, for the dK/dV kernel that follows.  Scores and their gradients are formed again here rather than
 // passed on: dQ summed by atomics from the dK/dV kernel would save 2 of the 7
 // products of the two kernels, but with an order that changes from run to
-// run.  8192 tokens, 32 heads of 128: 690 us, 1.19 PFLOP/s, matrix cores 57%
+// run.  8192 tokens, 32 heads of 128: 680 us, 1.21 PFLOP/s, matrix cores 65%
 // busy (with one wave a SIMD, 1240 us).
 template <int DP, bool EXACT, int SPLIT>
 __global__ __launch_bounds__(256 * SPLIT, DP == 64 && SPLIT == 1 ? 4 : 2) void attention_dq_kernel(const AttnArgs a) {
@@ -542,8 +544,8 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 && SPLIT == 1 ? 4 : 2) void a
 // has registers to run ahead: in turn k it forms the scores of tile k, and
 // its exponentials run under the products of tile k - 1.  Three tiles in LDS:
 // k - 1 and k in use, k + 1 on its way.  8192 tokens, 32 heads of 128 over 8
-// key heads: 1000 us, 1.10 PFLOP/s, matrix cores 48% and the LDS about as
-// busy.  (4 waves of 512 registers that keep both sums 1300 us; 8 waves that
+// key heads: 980 us, 1.12 PFLOP/s, matrix cores 54% busy, the LDS (at 128
+// bytes a cycle) about as long.  (4 waves of 512 registers that keep both sums 1300 us; 8 waves that
 // each keep both sums, starved of registers for reads ahead, 1180 us.)
 template <int DP>
 struct DkvLds {
