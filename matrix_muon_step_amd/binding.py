@@ -800,15 +800,17 @@ def _lse_tensor(lse, heads, rows, device):
     return _same_device(device, lse, "lse")
 
 
-def _new_rows(shape, tokens, dim, device, dtype):
-    """An output with zeros in the rows that the call leaves alone (those
-    behind the packing's last sequence)."""
+def _new_heads(like, tokens):
+    """An output of the shape of `like`, contiguous, with zeros in the rows
+    that the call leaves alone (those behind the packing's last sequence), and
+    its muon_heads_t."""
     import torch
 
-    t = torch.empty(shape, device=device, dtype=dtype)
-    if shape[dim] > tokens:
-        t.narrow(dim, tokens, shape[dim] - tokens).zero_()
-    return t
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    rows, heads, dim = t.shape
+    if rows > tokens:
+        t[tokens:].zero_()
+    return t, muon_heads_t(t.data_ptr(), heads * dim, dim)
 
 
 def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, max_logit=None, stream=None):
@@ -841,11 +843,15 @@ def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, 
         logit_heads = max_logit.numel()
     with _on(device, stream) as st:
         if o is None:
-            o = _new_rows(q.shape, packing.tokens, 0, device, torch.bfloat16)
+            o, do = _new_heads(q, packing.tokens)
+        else:
+            do, device = _heads_tensor("o", o, rows, device, like=q)
         if lse is None:
-            lse = _new_rows((heads, rows), packing.tokens, 1, device, torch.float32)
-        do, device = _heads_tensor("o", o, rows, device, like=q)
-        device = _lse_tensor(lse, heads, rows, device)
+            lse = q.new_empty((heads, rows), dtype=torch.float32)
+            if rows > packing.tokens:
+                lse[:, packing.tokens:].zero_()
+        else:
+            device = _lse_tensor(lse, heads, rows, device)
         args = muon_attention_t(dq, dk, dv, do, lse.data_ptr(), lse.stride(0) if heads > 1 else rows,
                                 max_logit.data_ptr() if max_logit is not None else None, logit_heads, heads, kv_heads,
                                 head_dim, float(head_dim ** -0.5 if scale is None else scale))
@@ -870,8 +876,11 @@ def muon_attention_backward(do, q, k, v, o, lse, packing: MuonPacking, scale=Non
     with _on(device, stream) as st:
         outs = {}
         for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-            outs[name] = _new_rows(like.shape, packing.tokens, 0, device, torch.bfloat16) if t is None else t
-            views[name], device = _heads_tensor(name, outs[name], rows, device, like=like)
+            if t is None:
+                outs[name], views[name] = _new_heads(like, packing.tokens)
+            else:
+                outs[name] = t
+                views[name], device = _heads_tensor(name, t, rows, device, like=like)
         args = muon_attention_grad_t(views["q"], views["k"], views["v"], views["o"], views["do"], lse.data_ptr(),
                                      lse.stride(0) if heads > 1 else rows, views["dq"], views["dk"], views["dv"], heads,
                                      kv_heads, head_dim, float(head_dim ** -0.5 if scale is None else scale))
@@ -967,8 +976,8 @@ def muon_checkpoint_write(xs, checkpoints=None, stream=None) -> List[MuonCheckpo
         _matrix_view(x, f"item {k}: x")
     with _on(xs[0].device, stream) as st:
         if checkpoints is None:
-            checkpoints = [MuonCheckpoint(torch.empty(muon_checkpoint_bytes(*x.shape), dtype=torch.uint8, device=x.device),
-                                          *x.shape) for x in xs]
+            checkpoints = [MuonCheckpoint(x.new_empty(muon_checkpoint_bytes(*x.shape), dtype=torch.uint8), *x.shape)
+                           for x in xs]
         arr, _ = _checkpoint_items(xs, checkpoints)
         _check(lib().muon_checkpoint_write(arr, len(xs), ctypes.c_void_p(st.cuda_stream)))
     return list(checkpoints)
@@ -987,8 +996,7 @@ def muon_checkpoint_read(checkpoints, xs=None, dtype=None, stream=None) -> List:
         return []
     with _on(checkpoints[0].data.device, stream) as st:
         if xs is None:
-            xs = [torch.empty((c.tokens, c.cols), dtype=dtype or torch.bfloat16, device=c.data.device)
-                  for c in checkpoints]
+            xs = [c.data.new_empty((c.tokens, c.cols), dtype=dtype or torch.bfloat16) for c in checkpoints]
         arr, _ = _checkpoint_items(xs, checkpoints)
         _check(lib().muon_checkpoint_read(arr, len(checkpoints), ctypes.c_void_p(st.cuda_stream)))
     return list(xs)
