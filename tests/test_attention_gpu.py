@@ -123,6 +123,8 @@ def test_many_tiles(mm):
     check_forward(mm, lengths, 10, 10, 64)
     check_backward(mm, lengths, 10, 10, 64, behind=2)
     check_backward(mm, lengths, 16, 8, 40)
+    check_backward(mm, lengths, 20, 10, 40, behind=1)
+    check_backward(mm, lengths, 27, 9, 64, layout="fused")
 
 
 @pytest.mark.parametrize("lengths", [[1025], [1100, 3, 64], [1151, 0, 1], [2000]], ids=str)
