@@ -138,7 +138,8 @@ def check_grad(dy, x_held, got, old=None):
 
 
 GRADS = [(1, 1, 1, 0), (1, 300, 33, 0), (31, 7, 64, 0), (32, 256, 256, 0), (33, 255, 300, 0), (100, 257, 31, 3),
-         (777, 300, 257, 8), (640, 64, 520, 5), (2100, 130, 260, 0), (3001, 77, 100, 8), (4096, 256, 256, 0)]
+         (777, 300, 257, 8), (640, 64, 520, 5), (2100, 130, 260, 0), (3001, 77, 100, 8), (4096, 256, 256, 0),
+         (8192, 501, 300, 0), (6000, 520, 270, 8)]  # several tiles, each cut into many shares
 
 
 @pytest.mark.parametrize("tokens,outs,cols,pad", GRADS)
