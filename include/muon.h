@@ -438,8 +438,9 @@ muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_pa
  * >= -117 with max |x| <= 448 * 2^e over the block's finite values; each
  * value is held as the 8-bit number (4 exponent and 3 mantissa bits, e4m3)
  * nearest to x * 2^-e, ties to even, and stands for that number times 2^e:
- * off by at most 2^-4 of x, or by 2^(e-10) where |x| < 2^(e-6).  NaN and
- * infinities are held as NaN.  A held value is exact in bfloat16.
+ * off by at most 2^-4 of x, or by 2^(e-10) where |x| < 2^(e-6).  Magnitudes
+ * above 1.875 * 2^127 are held as that (the next such number would be 2^128),
+ * NaN and infinities as NaN.  A held value is exact in bfloat16.
  *   x         DEVICE, element (t, c) at x[t * x_stride + c], dtype MUON_F32 or
  *             MUON_BF16, aligned to its element; x_stride >= cols
  *   data      DEVICE, 256-byte aligned, muon_checkpoint_bytes(tokens, cols)

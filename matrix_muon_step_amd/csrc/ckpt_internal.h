@@ -20,6 +20,8 @@ constexpr int kCkTile = 32;
 constexpr int kCkBlockBytes = 1024;
 // The smallest exponent keeps every held value a normal bfloat16 number.
 constexpr int kCkMinExp = -117;
+// The exponent of the largest finite float32 inputs.
+constexpr int kCkMaxExp = 120;
 
 // One activation of a write or read launch: 32 x 256 of it per work-group.
 constexpr int kCkGroupCols = 256;

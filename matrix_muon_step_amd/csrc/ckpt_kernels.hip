@@ -4,8 +4,9 @@
 // integer >= -117 with max |x| <= 448 * 2^e over its finite values; each
 // value is held as the e4m3 number nearest to x * 2^-e (ties to even), so
 // the error is at most 2^-4 of the value, or half of 2^-9 * 2^e for values
-// below 2^-6 * 2^e.  NaN and infinities are held as NaN.  A held value has
-// four significant bits, so it is exact in bfloat16 and the gradient
+// below 2^-6 * 2^e; from 1.875 * 2^127 on it is held as that, the largest one
+// that float32 and bfloat16 can hold.  NaN and infinities are held as NaN.  A held
+// value has four significant bits, so it is exact in bfloat16 and the gradient
 //   G[o][c] = sum_t dY[t][o] X[t][c]
 // is a product of exact bfloat16 operands, accumulated in float32.
 #include "ckpt_internal.h"
@@ -133,6 +134,13 @@ __device__ __forceinline__ void write_group(const CkDesc& d, int R, int group, L
     // 448 = 1.75 * 2^8
     const int e = max((top >> 23) - 135 + ((top & 0x7fffff) > 0x600000 ? 1 : 0), kCkMinExp);
     const float mul = __int_as_float((127 - e) << 23);
+    // At the largest exponent the code after 240 would stand for 2^128, which
+    // is no float32 number: what would round up to it keeps 240.
+    if (e == kCkMaxExp) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (fabsf(x[k]) > 0x1.ep127f) x[k] = copysignf(0x1.ep127f, x[k]);
+    }
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
