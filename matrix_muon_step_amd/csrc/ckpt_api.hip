@@ -114,13 +114,14 @@ constexpr int64_t kUnits = 256;  // compute units
 //   the work in 256-tiles cut into equal shares, one to a unit: 1.0 a step
 //     with every unit busy, the pieces (256 KB each, written and read, at 4.5
 //     TB/s) and a second launch (1600 x 6400: 404)
+// Matrices without tokens (experts that none was routed to) do not count: a
+// launch of either kind stores their zeros.
 GradPlan plan_grad(const muon_checkpoint_grad_t* mats, int64_t n) {
   int64_t tiles_of[kNumGradCfg] = {0, 0}, work[kNumGradCfg] = {0, 0}, longest = 0;
-  bool empty = false;
   for (int64_t i = 0; i < n; ++i) {
     const int64_t steps = tiles(mats[i].tokens, kCkTile);
+    if (steps == 0) continue;
     longest = std::max(longest, steps);
-    empty = empty || (steps == 0 && !mats[i].accumulate);
     for (int c = 0; c < kNumGradCfg; ++c) {
       const int64_t t = tiles(mats[i].outs, kGradTile[c]) * tiles(mats[i].cols, kGradTile[c]);
       tiles_of[c] += t;
@@ -144,11 +145,6 @@ GradPlan plan_grad(const muon_checkpoint_grad_t* mats, int64_t n) {
       p.share = tiles(work[kGrad256], parts);
       p.parts = tiles(work[kGrad256], p.share);
     }
-  }
-  if (empty && p.parts == 0) {  // tiles without steps are written by the joining pass
-    p.cfg = kGrad256;
-    p.share = std::max<int64_t>(1, tiles(work[kGrad256], kUnits));
-    p.parts = std::max<int64_t>(1, tiles(work[kGrad256], p.share));
   }
   if (p.parts) p.bytes = align_up(static_cast<size_t>(p.parts) * 2 * kGradTile[p.cfg] * kGradTile[p.cfg] * sizeof(float));
   return p;
@@ -256,7 +252,7 @@ muon_status_t muon_checkpoint_grad(const muon_checkpoint_grad_t* mats, int64_t n
       for (int64_t i = i0; i < i0 + count; ++i) {
         const muon_checkpoint_grad_t& m = mats[i];
         if (m.tokens == 0 && m.accumulate) continue;
-        aligned = aligned && reinterpret_cast<uintptr_t>(m.dy) % 16 == 0 && m.dy_stride % 8 == 0;
+        if (m.tokens > 0) aligned = aligned && reinterpret_cast<uintptr_t>(m.dy) % 16 == 0 && m.dy_stride % 8 == 0;
         GradDesc& d = b.d[b.n];
         d.dy = static_cast<const unsigned char*>(m.dy);
         d.dy_stride = m.dy_stride;
@@ -277,8 +273,7 @@ muon_status_t muon_checkpoint_grad(const muon_checkpoint_grad_t* mats, int64_t n
         ++b.n;
       }
       if (b.n == 0) continue;
-      hipError_t e = hipSuccess;
-      if (b.parts == 0 || b.steps[b.n] > 0) e = launch_ckpt_grad(b, plan.cfg, aligned, s);
+      hipError_t e = launch_ckpt_grad(b, plan.cfg, aligned, s);
       if (e == hipSuccess && b.parts) e = launch_grad_join(b, s);
       if (e != hipSuccess) return hip_fail(e, "gradient launch");
     }

@@ -342,7 +342,7 @@ __device__ __forceinline__ void grad_store(const GradDesc& d, int row0, int col0
     }
 }
 
-// Steps s0 .. s1 - 1 of the tile at (m0, n0) of G.
+// Steps s0 .. s1 - 1 of the tile at (m0, n0) of G; zeros where there are none.
 template <class C, bool ALIGNED>
 __device__ __forceinline__ void grad_tile(const GradDesc& d, int m0, int n0, int s0, int s1, LAS unsigned char* lds, int wave,
                                           int lane, f32x16_t (&acc)[C::MB][C::NB]) {
@@ -417,7 +417,7 @@ __device__ __forceinline__ void grad_tile(const GradDesc& d, int m0, int n0, int
         ld.direct(lds + fill, wave, lane);
         fill = next(fill);
       }
-  } else {
+  } else if (n > 0) {
     fetch();
     ld.blocks(lds, wave, lane);
     put(0);

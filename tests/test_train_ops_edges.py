@@ -1,0 +1,37 @@
+"""Edges of the training-step operators on the host (no GPU)."""
+import ctypes
+
+import pytest
+
+import matrix_muon_step_amd as mm
+from test_train_ops_abi import BASE, grad
+
+from matrix_muon_step_amd import binding as bd
+
+
+# ------------------------------------------------- gradients without tokens among others
+def workspace(*mats):
+    arr = (bd.muon_checkpoint_grad_t * len(mats))(*mats)
+    need = mm.lib().muon_checkpoint_grad_workspace_bytes(arr, len(mats))
+    assert mm.muon_last_error() == ""
+    return need
+
+
+SETS = {"tiles": [dict(tokens=777, cols=7168, outs=2048, dy_stride=2048)],
+        "small": [dict(tokens=40, cols=100, outs=60)] * 3,
+        "shares": [dict(tokens=16384, cols=1600, outs=6400, dy_stride=6400)],
+        "both": [dict(tokens=8192, cols=300, outs=501, dy_stride=501), dict(tokens=100, cols=256, outs=256, dy_stride=256)]}
+
+
+@pytest.mark.parametrize("name", SETS)
+@pytest.mark.parametrize("accumulate", [0, 1])
+@pytest.mark.parametrize("size", [dict(cols=7168, outs=2048, dy_stride=2048), dict(cols=65536, outs=65536, dy_stride=65536)],
+                         ids=["expert", "largest"])
+def test_a_gradient_without_tokens_changes_no_layout(name, accumulate, size):
+    """The workspace follows the layout: a matrix of no tokens (an expert that
+    none was routed to) leaves it as it is, wherever it stands."""
+    mats = [grad(accumulate=accumulate, **m) for m in SETS[name]]
+    none = grad(tokens=0, accumulate=accumulate, **size)
+    want = workspace(*mats)
+    assert workspace(none, *mats) == workspace(*mats, none) == workspace(mats[0], none, *mats[1:]) == want
+    assert workspace(none, none) == 0

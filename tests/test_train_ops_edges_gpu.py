@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_checkpoint_gpu import code_values, np64
+from test_checkpoint_gpu import activation, check_grad, code_values, np64, upstream
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,55 @@ def test_largest_values_stay_finite(mm, top):
     t[5, 5], t[6, 6], t[7, 7] = math.nan, math.inf, -math.inf
     got = np64(mm.muon_checkpoint_read(mm.muon_checkpoint_write([t]))[0])
     assert np.isnan(got[[5, 6, 7], [5, 6, 7]]).all() and np.isnan(got).sum() == 3
+
+
+# ------------------------------------------------- gradients without tokens among others
+def grad_set(mm, sizes, pad, g_type, seed=0):
+    mats = []
+    for i, (tokens, outs, cols) in enumerate(sizes):
+        saved = mm.muon_checkpoint_write([activation(max(tokens, 1), cols, BF16, seed=seed + i)[:tokens]])[0]
+        dy = upstream(max(tokens, 1), outs, pad, seed=seed + i)[:tokens]
+        mats.append((dy, saved, torch.full((outs, cols), math.nan, dtype=g_type, device="cuda")))
+    return mats
+
+
+SETS = [[(777, 300, 257), (640, 64, 520)],             # a work-group per tile
+        [(8192, 501, 300)],                             # tiles cut into shares
+        [(100, 256, 256), (33, 40, 700), (31, 264, 96)]]
+EMPTY = [(0, 24, 40), (0, 300, 257), (0, 7, 513)]
+
+
+@pytest.mark.parametrize("pad", [0, 8])
+@pytest.mark.parametrize("g_type", [F32, BF16])
+@pytest.mark.parametrize("which", range(len(SETS)))
+def test_empty_gradients_among_others(mm, which, g_type, pad):
+    """First, in the middle and last: zeros, and the others' bits unchanged."""
+    print(f"[case] gradients {SETS[which]} with empty ones {g_type} pad {pad}", flush=True)
+    mats = grad_set(mm, SETS[which], pad, g_type)
+    mm.muon_checkpoint_grad(mats)
+    want = [G.clone() for _, _, G in mats]
+    for (dy, saved, G) in mats:
+        check_grad(dy, np64(mm.muon_checkpoint_read([saved], dtype=F32)[0]), G)
+    empty = grad_set(mm, EMPTY, pad, g_type)
+    mixed = [empty[0], mats[0], empty[1], *mats[1:], empty[2]]
+    for _, _, G in mixed:
+        G.fill_(math.nan)
+    mm.muon_checkpoint_grad(mixed)
+    assert all((G == 0).all() for _, _, G in empty)
+    assert all(torch.equal(G, w) for (_, _, G), w in zip(mats, want))
+    for _, _, G in empty:
+        G.fill_(3.0)
+    old = [np64(G) for _, _, G in mats]
+    mm.muon_checkpoint_grad(mixed, accumulate=True)
+    assert all((G == 3).all() for _, _, G in empty)
+    for (dy, saved, G), o in zip(mats, old):
+        check_grad(dy, np64(mm.muon_checkpoint_read([saved], dtype=F32)[0]), G, o)
+
+
+@pytest.mark.parametrize("outs", [8, 7, 300])
+def test_only_empty_gradients(mm, outs):
+    print(f"[case] {outs} outs of no tokens", flush=True)
+    mats = grad_set(mm, [(0, outs, 40), (0, outs, 700)], 0, F32)
+    assert mm.muon_checkpoint_grad_workspace_bytes(mats) == 0
+    mm.muon_checkpoint_grad(mats)
+    assert all((G == 0).all() for _, _, G in mats)
