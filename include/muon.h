@@ -382,7 +382,8 @@ typedef struct muon_heads {
  *              the latter is what muon_qk_clip takes for a grouped layout
  *              (query projection with head_dim * heads / kv_heads rows per
  *              entry, key projection with head_dim).  A NaN logit gives
- *              NaN, +infinity where the row's largest logit is that.
+ *              NaN, +infinity where the row's largest logit is that; an entry
+ *              that is NaN stays NaN.
  *   heads      a multiple of kv_heads >= 1, at most MUON_MAX_HEADS; times the
  *              128-row pieces of the packing's sequences (the last of each may
  *              be shorter) below MUON_MAX_ATTENTION_ITEMS

@@ -245,11 +245,13 @@ __device__ __forceinline__ void store_rows(const HeadsView& v, int64_t row, int 
 // Running maximum of a float in memory, in any order of arrival with the
 // same result: for values >= 0 the integer order of the bits is the float
 // order, for negative ones the reverse.  NaN is passed as 0x7fffffff, which
-// both orders keep.  The value only grows, so one that is seen to have it
+// both orders keep; a NaN that the caller's array holds (of either sign) stays.
+// The value only grows, so one that is seen to have it
 // already (even an old one) needs no atomic: without that look, the 3800
 // atomics of a 4100-token call on 25 neighbouring floats cost 15 of its 42 us.
 __device__ __forceinline__ void atomic_max_float(float* p, float x) {
-  if (x <= __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) return;
+  const float old = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (x <= old || old != old) return;
   const int b = x != x ? 0x7fffffff : __float_as_int(x);
   if (b >= 0) atomicMax(reinterpret_cast<int*>(p), b);
   else atomicMin(reinterpret_cast<unsigned int*>(p), static_cast<unsigned int>(b));

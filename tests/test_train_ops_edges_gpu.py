@@ -120,3 +120,21 @@ def test_only_empty_gradients(mm, outs):
     assert mm.muon_checkpoint_grad_workspace_bytes(mats) == 0
     mm.muon_checkpoint_grad(mats)
     assert all((G == 0).all() for _, _, G in mats)
+
+
+# ------------------------------------------------------------ largest logits
+def test_max_logit_entry_that_is_nan(mm):
+    """A NaN of either sign in max_logit stays one, whatever the logits' sign."""
+    print("[case] max_logit with NaN entries", flush=True)
+    D = 64
+    p = mm.muon_packing_create([5])
+    q = torch.ones((5, 4, D), dtype=BF16, device="cuda")
+    k = torch.ones((5, 4, D), dtype=BF16, device="cuda")
+    k[:, 2:] = -1.0
+    bits = np.array([0xFFC00000, 0x7FC00000, 0xFFC00000, 0x7F800001], dtype=np.uint32).view(np.int32)
+    top = torch.from_numpy(bits).cuda().view(F32)
+    mm.muon_attention(q, k, q, p, max_logit=top)
+    assert torch.isnan(top).all(), top
+    per_group = torch.from_numpy(bits[:2].copy()).cuda().view(F32)
+    mm.muon_attention(q, k[:, 1:3], q[:, :2], p, max_logit=per_group)
+    assert torch.isnan(per_group).all(), per_group
