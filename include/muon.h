@@ -388,7 +388,9 @@ typedef struct muon_heads {
  *              128-row pieces of the packing's sequences (the last of each may
  *              be shorter) below MUON_MAX_ATTENTION_ITEMS
  *   head_dim   a multiple of 8, 8..128 (others: MUON_ERR_UNSUPPORTED)
- *   scale      finite, > 0
+ *   scale      finite, > 0; scale * log2(e) finite too (others:
+ *              MUON_ERR_UNSUPPORTED)
+ * Logits from 2^128 / log2(e) on, in magnitude, count as infinite in o and lse.
  * Rows of o and lse behind the packing's last sequence are left as they
  * were, and rows of q, k, v there are not read.  Sequences do not mix: a NaN
  * or infinity in a sequence reaches rows of that sequence only (there it

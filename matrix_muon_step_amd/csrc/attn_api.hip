@@ -60,6 +60,8 @@ muon_status_t check_shape(int32_t heads, int32_t kv_heads, int32_t head_dim, flo
   if (head_dim < 8 || head_dim > kAttnMaxDim || head_dim % 8 != 0)
     return fail(MUON_ERR_UNSUPPORTED, "muon: head_dim must be a multiple of 8 from 8 to 128");
   if (!finite(scale) || !(scale > 0.f)) return fail(MUON_ERR_INVALID_ARG, "muon: scale must be finite and > 0");
+  // the kernels' exponentials are of base 2
+  if (!finite(scale * kAttnLog2e)) return fail(MUON_ERR_UNSUPPORTED, "muon: scale * log2(e) is no float32 number");
   // a launch takes fewer than 2^32 lanes, a work-group up to 512
   if (packing->n_tiles * heads >= MUON_MAX_ATTENTION_ITEMS)
     return fail(MUON_ERR_UNSUPPORTED, "muon: too many work items (128-row pieces of the sequences x heads)");

@@ -12,6 +12,7 @@ constexpr int kAttnRows = 128;
 // Rows of the tiles that stream through LDS past a work item.
 constexpr int kAttnStep = 64;
 constexpr int kAttnMaxDim = 128;
+constexpr float kAttnLog2e = 1.44269504088896340736f;
 
 // One work item of a packing: rows first .. first + min(kAttnRows, len -
 // first) - 1 of the sequence that starts at packed row `row0`.

@@ -39,7 +39,6 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 #define LAS __attribute__((address_space(3)))
 
-constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
 // The rows' reference maximum moves only when a row outgrows it by 2^8:
@@ -339,7 +338,7 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
   const int turns = (min(t.len, t.first + kAttnRows) + SPLIT * kAttnStep - 1) / (SPLIT * kAttnStep);
   const int wq0 = t.first + 32 * (wave & 3);   // the wave's first query row in its sequence
   const int q = wq0 + (lane & 31);
-  const float c = a.scale * kLog2e;
+  const float c = a.scale * kAttnLog2e;
   const float slack = kSlackLog2 / c;
 
   KS stream(a, t, kv, wave, lane);
@@ -466,7 +465,7 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 && SPLIT == 1 ? 4 : 2) void a
   const int q = wq0 + (lane & 31);
   const bool live = q < t.len;
   const int64_t row = static_cast<int64_t>(t.row0) + q;
-  const float c = a.scale * kLog2e;
+  const float c = a.scale * kAttnLog2e;
 
   KS stream(a, t, kv, wave, lane);
   const FragOff fo = frag_offsets(lane);
@@ -485,7 +484,7 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 && SPLIT == 1 ? 4 : 2) void a
       for (int e = 0; e < 8; ++e) delta = fmaf(static_cast<float>(gf[s][e]), static_cast<float>(of[s][e]), delta);
     delta = half_sum(delta);
   }
-  const float lse2 = live ? gld<float>(a.lse + head * a.lse_stride + row) * kLog2e : 0.f;
+  const float lse2 = live ? gld<float>(a.lse + head * a.lse_stride + row) * kAttnLog2e : 0.f;
   if (live && h == 0 && part == 0) {
     gst(a.row_lse2 + head * a.row_stride + row, lse2);
     gst(a.row_delta + head * a.row_stride + row, delta);
@@ -686,7 +685,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
   const int total = nq * group;
   const int wk0 = t.first + 32 * (wave & 3), half = wave >> 2;
   const int key = wk0 + (lane & 31);
-  const float c = a.scale * kLog2e;
+  const float c = a.scale * kAttnLog2e;
 
   const FragOff fo = frag_offsets(lane);
   QueryStream<DP, EXACT, 8> stream(a, t, kv, nq, wave, lane);
@@ -773,7 +772,7 @@ __global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a)
   const int total = nq * (a.heads / a.kv_heads);
   const int wk0 = t.first + 32 * wave;
   const int key = wk0 + (lane & 31);
-  const float c = a.scale * kLog2e;
+  const float c = a.scale * kAttnLog2e;
   const FragOff fo = frag_offsets(lane);
   QueryStream<DP, EXACT, 4> stream(a, t, kv, nq, wave, lane);
   int q0 = stream.row, head = 0, cur = 0;

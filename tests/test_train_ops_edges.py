@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 import matrix_muon_step_amd as mm
-from test_train_ops_abi import BASE, grad
+from test_train_ops_abi import backward, call_backward, call_forward, forward, grad
 
 from matrix_muon_step_amd import binding as bd
 
@@ -35,3 +35,16 @@ def test_a_gradient_without_tokens_changes_no_layout(name, accumulate, size):
     want = workspace(*mats)
     assert workspace(none, *mats) == workspace(*mats, none) == workspace(mats[0], none, *mats[1:]) == want
     assert workspace(none, none) == 0
+
+
+# ------------------------------------------------------------ scales
+@pytest.mark.parametrize("make,call", [(forward, call_forward), (backward, call_backward)], ids=["forward", "backward"])
+def test_scales_without_a_base_two_form_are_refused(make, call):
+    """scale * log2(e) has to be a float32 number: with an infinite one a logit of 0 is NaN."""
+    a = make()
+    for scale in (2.36e38, 3.4e38):                    # 2^128 / log2(e) is 2.3586e38
+        a.scale = scale
+        assert call(a) == mm.MUON_ERR_UNSUPPORTED and "scale" in mm.muon_last_error()
+    for scale in (2.35e38, 1e-45):                     # pass on to the device check
+        a.scale = scale
+        assert call(a) in (mm.MUON_ERR_HIP, mm.MUON_ERR_INVALID_ARG) and "scale" not in mm.muon_last_error()
