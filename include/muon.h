@@ -476,7 +476,9 @@ muon_status_t muon_checkpoint_read(const muon_checkpoint_t* items, int64_t n, vo
  * sums, one rounding to G's type.
  *   dy    DEVICE bfloat16, element (t, o) at dy[t * dy_stride + o], 2-byte
  *         aligned, dy_stride >= outs and <= MUON_MAX_TOKEN_STRIDE (a 16-byte
- *         aligned dy with a stride that is a multiple of 8 is read fastest)
+ *         aligned dy with a stride that is a multiple of 8 is read fastest;
+ *         there, with outs odd, the four aligned bytes that hold dy's last
+ *         element are read whole)
  *   data  a checkpoint of (tokens, cols); matrices of a call may share it
  *   G     DEVICE, outs x cols row-major, MUON_F32 or MUON_BF16, 16-byte
  *         aligned, overlapping nothing else of the call

@@ -357,9 +357,11 @@ __device__ __forceinline__ void grad_tile(const GradDesc& d, int m0, int n0, int
   // (the last block again past the last column: those columns of G are not stored)
   ld.xp = d.codes + (static_cast<int64_t>(s0) * d.blocks + min(n0 / kCkTile + wave, d.blocks - 1)) * kCkBlockBytes;
   ld.left = d.tokens - s0 * 32;
-  // whole 16-byte chunks (aligned: none crosses a page): what the last one holds
-  // past `outs` meets only rows of G that are not stored
-  ld.tail = (width * 2 + 15) / 16 * 16;
+  // The loads' range is checked for each of a chunk's four words: in the last
+  // row they end with the word that holds the last element, the rest is zero.
+  // In other rows a chunk goes on past `outs`: those values meet only rows of G that
+  // are not stored.
+  ld.tail = (width * 2 + 3) / 4 * 4;
 #pragma unroll
   for (int i = 0; i < C::PA; ++i) ld.off[i] = static_cast<uint32_t>((k0 + i * C::ROWS) * ld.ld2 + ch * 16);
   // dY through registers: rows of any alignment.

@@ -122,6 +122,28 @@ def test_only_empty_gradients(mm, outs):
     assert all((G == 0).all() for _, _, G in mats)
 
 
+# ------------------------------------------------- the end of an aligned dY
+@pytest.mark.parametrize("outs", [1, 2, 3, 5, 6, 7, 9, 14, 70, 129, 250, 259])
+@pytest.mark.parametrize("tokens", [2, 32, 45, 1000, 6000])
+def test_grad_at_the_end_of_aligned_rows(mm, tokens, outs):
+    """Widths that end inside a 16-byte chunk: the last token's elements all
+    count, and nothing behind them does."""
+    print(f"[case] gradient {tokens} x {outs} x 40, aligned", flush=True)
+    stride = -(-outs // 8) * 8
+    x = activation(tokens, 40, BF16)
+    x[-1] = 1.0                                        # the last token counts as much as all others together
+    saved = mm.muon_checkpoint_write([x])[0]
+    xh = np64(mm.muon_checkpoint_read([saved], dtype=F32)[0])
+    room = torch.full((tokens + 2, stride), math.nan, dtype=BF16, device="cuda")
+    dy = room[1:tokens + 1, :outs]
+    dy.copy_(upstream(tokens, outs, 0))
+    dy[-1] = torch.arange(1, outs + 1, device="cuda").to(BF16)
+    assert dy.data_ptr() % 16 == 0
+    G = torch.full((outs, 40), math.nan, device="cuda")
+    mm.muon_checkpoint_grad([(dy, saved, G)])
+    check_grad(dy, xh, G)
+
+
 # ------------------------------------------------------------ largest logits
 def test_max_logit_entry_that_is_nan(mm):
     """A NaN of either sign in max_logit stays one, whatever the logits' sign."""
