@@ -826,7 +826,10 @@ def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, 
     the largest scaled logit of its heads in this call: start it at -inf once
     per optimizer step, pass it to every call of the layer, then hand it to
     muon_qk_clip (with one entry per key head, the query projection's head_dim
-    there is head_dim * heads // kv_heads)."""
+    there is head_dim * heads // kv_heads).
+
+    stream: as for muon_step; the caller keeps tensors of another stream until
+    the call has finished on this one (the packing keeps its own memory)."""
     import torch
 
     rows = _attention_rows(q, k, v, packing)
@@ -864,7 +867,8 @@ def muon_attention_backward(do, q, k, v, o, lse, packing: MuonPacking, scale=Non
     """Gradients (dq, dk, dv) of muon_attention, bfloat16, from the upstream
     gradient `do` and what the forward call took and returned.  As there,
     rows behind the last sequence stay as they are in outputs given by the
-    caller and are zero in outputs made here."""
+    caller and are zero in outputs made here, and the caller keeps tensors of
+    another stream until the call has finished."""
     import torch
 
     rows = _attention_rows(q, k, v, packing)
@@ -898,13 +902,22 @@ def muon_attention_backward(do, q, k, v, o, lse, packing: MuonPacking, scale=Non
 
 class MuonCheckpoint:
     """An activation held in 8 bits (muon_checkpoint_write): `data` (uint8,
-    an opaque layout), `tokens`, `cols`."""
+    an opaque layout), `tokens`, `cols`.  One that muon_checkpoint_write made
+    may be used on any stream ordered after that call and dropped while such a
+    use is under way; data of the caller's own has to be kept until then."""
 
     def __init__(self, data, tokens, cols):
         self.data = data
         self.tokens = int(tokens)
         self.cols = int(cols)
         self._need = 0  # bytes, once asked for
+        self._stream = None  # made here: the stream that the data's memory belongs to
+
+    def _used_on(self, stream):
+        """After a call on `stream` the data's memory is not handed out again
+        before that stream is done with it."""
+        if self._stream is not None and stream.cuda_stream != self._stream:
+            self.data.record_stream(stream.torch_stream() if isinstance(stream, _current) else stream)
 
     def _bytes(self):
         if not self._need:
@@ -978,7 +991,11 @@ def muon_checkpoint_write(xs, checkpoints=None, stream=None) -> List[MuonCheckpo
         if checkpoints is None:
             checkpoints = [MuonCheckpoint(x.new_empty(muon_checkpoint_bytes(*x.shape), dtype=torch.uint8), *x.shape)
                            for x in xs]
+            for c in checkpoints:
+                c._stream = st.cuda_stream
         arr, _ = _checkpoint_items(xs, checkpoints)
+        for c in checkpoints:
+            c._used_on(st)
         _check(lib().muon_checkpoint_write(arr, len(xs), ctypes.c_void_p(st.cuda_stream)))
     return list(checkpoints)
 
@@ -998,6 +1015,8 @@ def muon_checkpoint_read(checkpoints, xs=None, dtype=None, stream=None) -> List:
         if xs is None:
             xs = [c.data.new_empty((c.tokens, c.cols), dtype=dtype or torch.bfloat16) for c in checkpoints]
         arr, _ = _checkpoint_items(xs, checkpoints)
+        for c in checkpoints:
+            c._used_on(st)
         _check(lib().muon_checkpoint_read(arr, len(checkpoints), ctypes.c_void_p(st.cuda_stream)))
     return list(xs)
 
@@ -1036,7 +1055,8 @@ def muon_checkpoint_grad(matrices, accumulate=False, workspace=None, stream=None
     checkpoint's held values, for dY (tokens, outs) bfloat16 with contiguous
     rows and G (outs, cols) float32 or bfloat16, contiguous: the G of
     muon_step.  Matrices may share a checkpoint (query, key and value
-    projections do).  accumulate adds to G instead."""
+    projections do).  accumulate adds to G instead.  The caller keeps dY and G
+    of another stream until the call has finished on this one."""
     matrices = list(matrices)
     if not matrices:
         return
@@ -1048,4 +1068,6 @@ def muon_checkpoint_grad(matrices, accumulate=False, workspace=None, stream=None
         if workspace is None:
             workspace = _alloc_workspace(need, device)
         ws_ptr, ws_len = _ws_args(workspace, device)
+        for _, c, _ in matrices:
+            c._used_on(st)
         _check(lib().muon_checkpoint_grad(arr, len(matrices), ws_ptr, ws_len, ctypes.c_void_p(st.cuda_stream)))

@@ -160,3 +160,40 @@ def test_max_logit_entry_that_is_nan(mm):
     per_group = torch.from_numpy(bits[:2].copy()).cuda().view(F32)
     mm.muon_attention(q, k[:, 1:3], q[:, :2], p, max_logit=per_group)
     assert torch.isnan(per_group).all(), per_group
+
+
+# ------------------------------------------------------------------- streams
+@pytest.mark.parametrize("use", ["read", "write", "grad", "attention"])
+def test_memory_in_use_on_another_stream_is_not_handed_out(mm, use):
+    """A checkpoint or packing that is dropped while a call on another stream
+    is still to run keeps its memory until that call is done."""
+    print(f"[case] dropped while in use by {use}", flush=True)
+    tokens, cols = 5000, 300
+    x = activation(tokens, cols, BF16)
+    if use == "attention":
+        q = torch.ones((tokens, 2, 64), dtype=BF16, device="cuda")
+        made = mm.muon_packing_create([1] * tokens)
+        data = made._table
+    else:
+        made = mm.muon_checkpoint_write([x])[0]
+        data = made.data
+    at, size = data.data_ptr(), data.numel()
+    dy, G = upstream(tokens, 64, 0), torch.zeros((64, cols), device="cuda")
+    again = torch.empty_like(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)                  # what follows waits some 50 ms
+        if use == "read":
+            mm.muon_checkpoint_read([made], xs=[again])
+        elif use == "write":
+            mm.muon_checkpoint_write([x], [made])
+        elif use == "grad":
+            mm.muon_checkpoint_grad([(dy, made, G)])
+        else:
+            mm.muon_attention(q, q, q, made)
+    del made, data
+    new = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert not side.query(), "the side stream was done too early to tell"
+    assert new.data_ptr() != at
+    torch.cuda.synchronize()
