@@ -394,7 +394,8 @@ class _on:
         if stream is None:
             index = torch.cuda.current_device()
             if device is None or device.index == index:
-                return _current(torch._C._cuda_getCurrentRawStream(index))
+                raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # not in torch's documented interface
+                return _current(raw(index)) if raw else torch.cuda.current_stream(index)
         with contextlib.ExitStack() as stack:  # undone if something here raises
             if device is not None:
                 stack.enter_context(torch.cuda.device(device))

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import matrix_muon_step_amd as mm
 from test_train_ops_abi import backward, call_backward, call_forward, forward, grad
@@ -48,3 +49,20 @@ def test_scales_without_a_base_two_form_are_refused(make, call):
     for scale in (2.35e38, 1e-45):                     # pass on to the device check
         a.scale = scale
         assert call(a) in (mm.MUON_ERR_HIP, mm.MUON_ERR_INVALID_ARG) and "scale" not in mm.muon_last_error()
+
+
+# ------------------------------------------------------------ the binding
+def test_current_stream_without_torch_internals(monkeypatch):
+    """Where torch lacks the call that gives the current stream's handle, its documented one serves."""
+    class Stream:
+        cuda_stream = 4711
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream() if device == 2 else None)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 4710 + index // 2, raising=False)
+    with bd._on(None, None) as st:
+        assert st.cuda_stream == 4711
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    for device in (None, torch.device("cuda", 2)):
+        with bd._on(device, None) as st:
+            assert st.cuda_stream == 4711
