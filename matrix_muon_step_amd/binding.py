@@ -911,7 +911,7 @@ class MuonCheckpoint:
         self.data = data
         self.tokens = int(tokens)
         self.cols = int(cols)
-        self._need = 0  # bytes, once asked for
+        self._need = (None, None, 0)  # tokens and cols that were asked for, and their bytes
         self._stream = None  # made here: the stream that the data's memory belongs to
 
     def _used_on(self, stream):
@@ -921,9 +921,9 @@ class MuonCheckpoint:
             self.data.record_stream(stream.torch_stream() if isinstance(stream, _current) else stream)
 
     def _bytes(self):
-        if not self._need:
-            self._need = muon_checkpoint_bytes(self.tokens, self.cols)
-        return self._need
+        if self._need[:2] != (self.tokens, self.cols):
+            self._need = (self.tokens, self.cols, muon_checkpoint_bytes(self.tokens, self.cols))
+        return self._need[2]
 
 
 def muon_checkpoint_bytes(tokens: int, cols: int) -> int:

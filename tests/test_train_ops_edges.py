@@ -66,3 +66,19 @@ def test_current_stream_without_torch_internals(monkeypatch):
     for device in (None, torch.device("cuda", 2)):
         with bd._on(device, None) as st:
             assert st.cuda_stream == 4711
+
+
+def test_checkpoint_size_follows_its_fields():
+    """The check of the data's size is that of the tokens and columns that the call will use."""
+    c = mm.MuonCheckpoint(None, 32, 32)
+    assert c._bytes() == mm.muon_checkpoint_bytes(32, 32)
+    c.tokens = 320
+    assert c._bytes() == mm.muon_checkpoint_bytes(320, 32)
+    c.cols = 64
+    assert c._bytes() == c._bytes() == mm.muon_checkpoint_bytes(320, 64)
+    c.tokens = -1
+    with pytest.raises(mm.MuonError):
+        c._bytes()
+    empty = mm.MuonCheckpoint(None, 0, 0)
+    with pytest.raises(mm.MuonError):
+        empty._bytes()
