@@ -740,12 +740,21 @@ class MuonPacking:
             pass
 
 
+def _int64(n, what):
+    """A whole number that the library's 64 bits hold (ctypes would cut a larger
+    one without a word, int() a fraction)."""
+    whole = int(n)
+    if whole != n or not -(1 << 63) <= whole < 1 << 63:
+        raise ValueError(f"{what} must be a whole number of 64 bits")
+    return whole
+
+
 def muon_packing_create(lengths: Sequence[int], device=None, stream=None) -> MuonPacking:
     """The packing of sequences of these lengths (host integers >= 0) on
     `device` (default: the current one).  Waits for `stream`."""
     import torch
 
-    lengths = [int(n) for n in lengths]
+    lengths = [_int64(n, "a packing length") for n in lengths]
     arr = (ctypes.c_int64 * max(1, len(lengths)))(*lengths)
     need = int(lib().muon_packing_bytes(arr, len(lengths)))
     if need == 0:
@@ -927,7 +936,7 @@ class MuonCheckpoint:
 
 
 def muon_checkpoint_bytes(tokens: int, cols: int) -> int:
-    nbytes = int(lib().muon_checkpoint_bytes(int(tokens), int(cols)))
+    nbytes = int(lib().muon_checkpoint_bytes(_int64(tokens, "tokens"), _int64(cols, "cols")))
     if nbytes == 0:
         raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error())
     return nbytes

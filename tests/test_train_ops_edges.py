@@ -1,6 +1,7 @@
 """Edges of the training-step operators on the host (no GPU)."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -82,3 +83,19 @@ def test_checkpoint_size_follows_its_fields():
     empty = mm.MuonCheckpoint(None, 0, 0)
     with pytest.raises(mm.MuonError):
         empty._bytes()
+
+
+@pytest.mark.parametrize("n", [(1 << 64) + 5, 5 - (1 << 64), 1 << 63, 3.7, 1e30, float("nan"), "7"])
+def test_numbers_that_64_bits_do_not_hold(n):
+    """Neither their low bits nor their whole part is taken for them."""
+    with pytest.raises(ValueError):
+        mm.muon_packing_create([3, n])
+    with pytest.raises(ValueError):
+        mm.muon_checkpoint_bytes(n, 5)
+    with pytest.raises(ValueError):
+        mm.muon_checkpoint_bytes(5, n)
+
+
+def test_numbers_of_other_integer_types():
+    for n in (np.int32(33), torch.tensor(33), 33.0):
+        assert mm.muon_checkpoint_bytes(n, n) == mm.muon_checkpoint_bytes(33, 33)
