@@ -760,6 +760,8 @@ def muon_packing_create(lengths: Sequence[int], device=None, stream=None) -> Muo
     if need == 0:
         raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error())
     device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError(f"a packing cannot be on {device}")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     with _on(device, stream) as st:

@@ -99,3 +99,11 @@ def test_numbers_that_64_bits_do_not_hold(n):
 def test_numbers_of_other_integer_types():
     for n in (np.int32(33), torch.tensor(33), 33.0):
         assert mm.muon_checkpoint_bytes(n, n) == mm.muon_checkpoint_bytes(33, 33)
+
+
+def test_packings_are_on_gpus_only(monkeypatch):
+    """"cpu" is not taken for the current GPU."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: pytest.fail("went on to a GPU"))
+    for device in ("cpu", torch.device("cpu"), "meta"):
+        with pytest.raises(ValueError):
+            mm.muon_packing_create([3], device=device)
