@@ -445,7 +445,8 @@ muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_pa
  * above 1.875 * 2^127 are held as that (the next such number would be 2^128),
  * NaN and infinities as NaN.  A held value is exact in bfloat16.
  *   x         DEVICE, element (t, c) at x[t * x_stride + c], dtype MUON_F32 or
- *             MUON_BF16, aligned to its element; x_stride >= cols
+ *             MUON_BF16, aligned to its element; x_stride >= cols, at most 2^40,
+ *             and tokens * x_stride at most 2^56
  *   data      DEVICE, 256-byte aligned, muon_checkpoint_bytes(tokens, cols)
  *             bytes (cols and tokens rounded up to 32, plus 1 / 1024); an
  *             opaque layout, made for muon_checkpoint_grad

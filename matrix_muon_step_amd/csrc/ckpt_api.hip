@@ -45,7 +45,9 @@ muon_status_t move_all(const muon_checkpoint_t* items, int64_t n, bool write, vo
     if (m.x_dtype != MUON_F32 && m.x_dtype != MUON_BF16)
       return fail(MUON_ERR_INVALID_ARG, id + ": x_dtype must be MUON_F32 or MUON_BF16");
     if (m.x_stride < m.cols) return fail(MUON_ERR_INVALID_ARG, id + ": x_stride is smaller than cols");
-    if (m.x_stride > (int64_t{1} << 40)) return fail(MUON_ERR_UNSUPPORTED, id + ": x_stride too large");
+    // (the extent in bytes stays far below 2^63)
+    if (m.x_stride > (int64_t{1} << 40) || m.x_stride > (int64_t{1} << 56) / std::max<int64_t>(1, m.tokens))
+      return fail(MUON_ERR_UNSUPPORTED, id + ": x_stride too large");
     if (m.tokens == 0) continue;
     if (tiles(m.tokens, kCkTile) * tiles(m.cols, kCkGroupCols) >= kMaxGroups)
       return fail(MUON_ERR_UNSUPPORTED, id + " is too large for one launch");

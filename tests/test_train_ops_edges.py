@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import matrix_muon_step_amd as mm
-from test_train_ops_abi import backward, call_backward, call_forward, forward, grad
+from test_train_ops_abi import backward, call_backward, call_forward, forward, grad, item
 
 from matrix_muon_step_amd import binding as bd
 
@@ -50,6 +50,19 @@ def test_scales_without_a_base_two_form_are_refused(make, call):
     for scale in (2.35e38, 1e-45):                     # pass on to the device check
         a.scale = scale
         assert call(a) in (mm.MUON_ERR_HIP, mm.MUON_ERR_INVALID_ARG) and "scale" not in mm.muon_last_error()
+
+
+# ------------------------------------------------------------ extents
+@pytest.mark.parametrize("tokens,stride", [(1 << 24, 1 << 40), (1 << 23, 1 << 40), (1 << 28, 1 << 35), (1 << 28, (1 << 28) + 1)])
+def test_extents_past_64_bits_are_refused(tokens, stride):
+    """An x whose extent in bytes wraps would pass the overlap checks."""
+    arr = (bd.muon_checkpoint_t * 1)(item(tokens=tokens, x_stride=stride, cols=8))
+    for f in (mm.lib().muon_checkpoint_write, mm.lib().muon_checkpoint_read):
+        assert f(arr, 1, None) == mm.MUON_ERR_UNSUPPORTED and "x_stride" in mm.muon_last_error()
+    # as far as it goes, the overlap is seen: data inside x
+    inside = item(tokens=1 << 16, x_stride=1 << 40, cols=8, data=item().x + (1 << 40))
+    arr = (bd.muon_checkpoint_t * 1)(inside)
+    assert mm.lib().muon_checkpoint_write(arr, 1, None) == mm.MUON_ERR_ALIAS
 
 
 # ------------------------------------------------------------ the binding
