@@ -212,9 +212,11 @@ def run(state):
     if case["op"] == "attention":
         if own:
             import matrix_muon_step_amd as mm
+            # raised in place by the call: each pass starts where the state does, like a step's first call
+            top = state["max_logit"].clone()
             o, lse = mm.muon_attention(state["q"], state["k"], state["v"], state["packing"], scale=state["scale"],
-                                       max_logit=state["max_logit"])
-            return dict(o=o[:T], lse=lse[:, :T], max_logit=state["max_logit"])
+                                       max_logit=top)
+            return dict(o=o[:T], lse=lse[:, :T], max_logit=top)
         o, lse, top = _plain_attention(state["q"], state["k"], state["v"], state["lens"], state["scale"])
         return dict(o=o.to(torch.bfloat16), lse=lse, max_logit=torch.maximum(state["max_logit"], top))
     if case["op"] == "backward":
