@@ -186,6 +186,15 @@ __device__ __forceinline__ void next_tile() {
   asm volatile("" ::: "memory");
 }
 
+// This wave's LDS accesses are behind it; past the barrier that holds for all
+// waves.  Stores to memory go on.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // x of lane l and of lane l ^ 32, the lower lane's first.
 __device__ __forceinline__ void halves(float x, float& lo, float& hi) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -245,9 +254,11 @@ __device__ __forceinline__ void store_rows(const HeadsView& v, int64_t row, int 
 // same result: for values >= 0 the integer order of the bits is the float
 // order, for negative ones the reverse.  NaN is passed as 0x7fffffff, which
 // both orders keep; a NaN that the caller's array holds (of either sign) stays.
-// The value only grows, so one that is seen to have it
-// already (even an old one) needs no atomic: without that look, the 3800
-// atomics of a 4100-token call on 25 neighbouring floats cost 15 of its 42 us.
+// The value only grows, so one that is seen to have it already (even an old
+// one) needs no atomic.  Atomics on neighbouring floats follow one another, about
+// 5 ns each: 4100 tokens in ten sequences, 25 heads of 64, from -infinity 43 us
+// with one a wave and 33 with one a work-group, 26 where the maxima are there
+// already or none are asked for; 64 x 64 tokens 44, 32 and 13.
 __device__ __forceinline__ void atomic_max_float(float* p, float x) {
   const float old = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   if (x <= old || old != old) return;
@@ -415,7 +426,13 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
       *(LAS f32x4_t*)(at + G::DB * 4096) = (f32x4_t){m_ref, m_top, l, 0.f};
     }
     next_tile();
-    if (part == 1) return;
+    if (part == 1) {
+      if (a.max_logit) {  // the barriers that the other waves come to below
+        lds_barrier();
+        lds_barrier();
+      }
+      return;
+    }
     const f32x4_t x = *(const LAS f32x4_t*)(at + G::DB * 4096);
     const float m = fmaxf(m_ref, x[0]), common = m == -kInf ? 0.f : m * c;
     // without a reference the sums are zero (or NaN): as they are
@@ -437,7 +454,16 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
       const float other = __shfl_xor(top, off, 64);
       top = top != top || other != other ? __builtin_nanf("") : fmaxf(top, other);
     }
-    if (lane == 0 && wq0 < t.len) atomic_max_float(a.max_logit + head / a.logit_group, top);
+    // one atomic for the work-group (rows past the sequence hold -infinity)
+    lds_barrier();
+    if (lane == 0) *(LAS float*)(lds + 4 * wave) = top;
+    lds_barrier();
+    if (threadIdx.x == 0) {
+      const f32x4_t x = *(const LAS f32x4_t*)lds;
+#pragma unroll
+      for (int w = 1; w < 4; ++w) top = top != top || x[w] != x[w] ? __builtin_nanf("") : fmaxf(top, x[w]);
+      atomic_max_float(a.max_logit + head / a.logit_group, top);
+    }
   }
 }
 

@@ -197,3 +197,22 @@ def test_memory_in_use_on_another_stream_is_not_handed_out(mm, use):
     assert not side.query(), "the side stream was done too early to tell"
     assert new.data_ptr() != at
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------ largest logits, wave by wave
+@pytest.mark.parametrize("n,D", [(300, 64), (1100, 64), (1100, 128)])
+def test_max_logit_in_any_row(mm, n, D):
+    """The largest logit counts whichever row of a work item has it (one head
+    for each 16th row), in short sequences and in split ones."""
+    print(f"[case] largest logit in any of {n} rows, heads of {D}", flush=True)
+    rows = list(range(0, n, 16)) + [n - 1]
+    H = len(rows)
+    q = torch.ones((n, H, D), dtype=BF16, device="cuda")
+    k = torch.ones((n, H, D), dtype=BF16, device="cuda")
+    for h, r in enumerate(rows):
+        q[r, h] = 1.0 + (h + 1) / 128.0 if h < 127 else 2.0
+    for heads in (1, 3, H):                            # few heads: split; many: not
+        want = [D * float(q[rows[h], h, 0]) for h in range(heads)]
+        top = torch.full((heads,), -math.inf, device="cuda")
+        mm.muon_attention(q[:, :heads], k[:, :heads], k[:, :heads], mm.muon_packing_create([n]), scale=1.0, max_logit=top)
+        np.testing.assert_array_equal(top.cpu().numpy(), np.array(want, dtype=np.float32))
