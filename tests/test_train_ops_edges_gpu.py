@@ -5,6 +5,8 @@ import numpy as np
 import pytest
 import torch
 
+import attention_ref as ref
+from test_attention_gpu import host, inputs
 from test_checkpoint_gpu import activation, check_grad, code_values, np64, upstream
 
 pytestmark = pytest.mark.gpu
@@ -216,3 +218,88 @@ def test_max_logit_in_any_row(mm, n, D):
         top = torch.full((heads,), -math.inf, device="cuda")
         mm.muon_attention(q[:, :heads], k[:, :heads], k[:, :heads], mm.muon_packing_create([n]), scale=1.0, max_logit=top)
         np.testing.assert_array_equal(top.cpu().numpy(), np.array(want, dtype=np.float32))
+
+
+def test_max_logit_next_to_the_largest_float(mm):
+    """Logits that are finite while their base-2 form is not: the largest is still theirs."""
+    print("[case] max_logit near 2^128", flush=True)
+    D = 64
+    p = mm.muon_packing_create([70])
+    q = torch.zeros((70, 3, D), dtype=BF16, device="cuda")
+    k = torch.zeros((70, 3, D), dtype=BF16, device="cuda")
+    q[:, 0, 3], k[66, 0, 3] = 2.0 ** 64, 2.0 ** 63     # 2^127 * 1.9 = 0.95 * 2^128
+    q[:, 1, 3], k[0, 1, 3] = 2.0 ** 64, 2.0 ** 62      # half of it: finite in base 2 too
+    q[:, 2, 3], k[5, 2, 3] = 2.0 ** 64, 2.0 ** 64      # infinite
+    top = torch.full((3,), -math.inf, device="cuda")
+    mm.muon_attention(q, k, torch.ones_like(q), p, scale=1.9, max_logit=top)
+    s = np.float32(1.9)
+    np.testing.assert_array_equal(top.cpu().numpy(), np.array([s * np.float32(2.0 ** 127), s * np.float32(2.0 ** 126), np.inf],
+                                                              dtype=np.float32))
+
+
+# ------------------------------------------- not finite, on every kernel variant
+# (lengths, heads, kv heads, head size): keys split over two wave groups, and
+# more key tiles than the pair kernel takes
+VARIANTS = {"split": ([1100, 40], 2, 2, 64), "split128": ([40, 1100], 4, 2, 128), "three": ([64] * 50 + [130], 11, 11, 64),
+            "three40": ([70] * 50 + [130], 11, 11, 40)}
+
+
+@pytest.mark.parametrize("name", VARIANTS)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_variants_keep_sequences_apart(mm, name, bad):
+    lens, H, K, D = VARIANTS[name]
+    print(f"[case] isolation {name} {bad}", flush=True)
+    T = sum(lens)
+    q, k, v, do = inputs(lens, H, K, D, behind=9, layout="plain")
+    p = mm.muon_packing_create(lens)
+    o, lse = mm.muon_attention(q, k, v, p)
+    grads = mm.muon_attention_backward(do, q, k, v, o, lse, p)
+    assert all(torch.isfinite(t).all() for t in (o[:T], lse[:, :T], *(g[:T] for g in grads)))
+    start = np.concatenate([[0], np.cumsum(lens)])
+    for seq in {0, len(lens) // 2, len(lens) - 1}:
+        for at in {0, lens[seq] // 2, lens[seq] - 1}:
+            row = int(start[seq]) + at
+            x = [t.clone() for t in (q, k, v, do)]
+            for t in x:
+                t[row, :, 5] = bad
+            o2, lse2 = mm.muon_attention(x[0], x[1], x[2], p)
+            g2 = mm.muon_attention_backward(x[3], x[0], x[1], x[2], o2, lse2, p)
+            for rows in (slice(0, int(start[seq])), slice(int(start[seq + 1]), None)):
+                assert torch.equal(o[rows], o2[rows]) and torch.equal(lse[:, rows], lse2[:, rows])
+                for a, b in zip(grads, g2):
+                    assert torch.equal(a[rows], b[rows])
+            assert not torch.isfinite(o2[row]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pos", [0, 10, 70, 700, 1000, 1050, 1099])
+def test_split_keys_not_finite_logits(mm, pos, D):
+    """One key of a long sequence gives a NaN, an infinite or a -infinite logit
+    (each in a head of its own), in a tile of either wave group: rows before it
+    and the largest logits follow the formulas."""
+    print(f"[case] split keys, key {pos} not finite, heads of {D}", flush=True)
+    n = 1100
+    p = mm.muon_packing_create([n])
+    q = torch.ones((n, 5, D), dtype=BF16, device="cuda")
+    k = -torch.ones((n, 5, D), dtype=BF16, device="cuda")
+    v = torch.ones((n, 5, D), dtype=BF16, device="cuda")
+    k[pos, 0, 3] = math.nan
+    k[pos, 1, 3] = math.inf
+    k[pos, 2, 3] = -math.inf
+    k[:, 3, 3] = -math.inf
+    top = torch.full((5,), -math.inf, device="cuda")
+    o, lse = mm.muon_attention(q, k, v, p, scale=0.5, max_logit=top)
+    got, one = lse.cpu().numpy().astype(np.float64), -0.5 * D
+    t = top.cpu().numpy()
+    # the base logit is exact; the one with an element of infinite size is that infinity
+    assert np.isnan(t[0]) and t[1] == np.inf and t[2] == one and t[3] == -np.inf and t[4] == one
+    i = np.arange(n)
+    count = {0: i + 1.0, 1: i + 1.0, 2: np.where(i >= pos, i, i + 1.0), 4: i + 1.0}
+    for h, c in count.items():
+        rows = i < pos if h < 2 else c > 0
+        want = one + np.log(c[rows])
+        # the logits are exact, their sum is a sum of ones: log2, a product and an addition in float32
+        assert (np.abs(got[h, rows] - want) <= 4 * ref.F32 * (np.abs(want) + 1) + 2.0 ** -20).all(), h
+        assert (host(o[:, h][torch.from_numpy(rows).cuda()], n) == 1).all(), h
+        assert np.isnan(got[h, ~rows]).all() if h < 2 else np.isneginf(got[h, ~rows]).all(), h
+    assert np.isneginf(got[3]).all()
