@@ -9,6 +9,7 @@ from .binding import (  # noqa: F401
     muon_orthogonalize_workspace_bytes, muon_orthogonalize, muon_plan_query,
     muon_profile_enable, muon_profile_read, muon_copy_probe, muon_qk_clip,
     MuonPacking, muon_packing_create, muon_attention, muon_attention_backward,
+    muon_attention_backward_workspace_bytes,
     MuonCheckpoint, muon_checkpoint_bytes, muon_checkpoint_write, muon_checkpoint_read,
     muon_checkpoint_grad_workspace_bytes, muon_checkpoint_grad, lib, LIB_PATH,
 )

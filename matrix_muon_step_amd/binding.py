@@ -715,11 +715,14 @@ class MuonPacking:
         self.tokens = sum(lengths)
         self.device = device
 
+    def _open(self):
+        if not self._h:
+            raise RuntimeError("the packing is closed")
+
     def _enter(self, device, stream):
         """The handle for a call on `stream`, after which the table's memory
         is not handed out again before that stream is done with it."""
-        if not self._h:
-            raise RuntimeError("the packing is closed")
+        self._open()
         if device is not None and device != self.device:
             raise ValueError(f"the packing is on {self.device}, the call's tensors on {device}")
         if stream.cuda_stream != self._stream:
@@ -874,13 +877,24 @@ def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, 
     return o, lse
 
 
+def muon_attention_backward_workspace_bytes(q, k, packing: MuonPacking) -> int:
+    """Bytes of the workspace that muon_attention_backward takes for such q and k."""
+    packing._open()
+    args = muon_attention_grad_t(heads=q.shape[1], kv_heads=k.shape[1], head_dim=q.shape[2], scale=1.0)
+    nbytes = int(lib().muon_attention_backward_workspace_bytes(ctypes.byref(args), ctypes.c_void_p(packing._h)))
+    if nbytes == 0:
+        raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error())
+    return nbytes
+
+
 def muon_attention_backward(do, q, k, v, o, lse, packing: MuonPacking, scale=None, dq=None, dk=None, dv=None,
                             workspace=None, stream=None):
     """Gradients (dq, dk, dv) of muon_attention, bfloat16, from the upstream
     gradient `do` and what the forward call took and returned.  As there,
     rows behind the last sequence stay as they are in outputs given by the
     caller and are zero in outputs made here, and the caller keeps tensors of
-    another stream until the call has finished."""
+    another stream until the call has finished.  workspace: a uint8 GPU tensor
+    of muon_attention_backward_workspace_bytes; made for the call by default."""
     import torch
 
     rows = _attention_rows(q, k, v, packing)

@@ -120,3 +120,21 @@ def test_packings_are_on_gpus_only(monkeypatch):
     for device in ("cpu", torch.device("cpu"), "meta"):
         with pytest.raises(ValueError):
             mm.muon_packing_create([3], device=device)
+
+
+def test_backward_workspace_by_its_shapes():
+    """What the library asks for, for an empty packing (the only one that needs
+    no GPU), and the refusals."""
+    table, h = (ctypes.c_char * 512)(), ctypes.c_void_p()
+    at = (ctypes.addressof(table) + 255) // 256 * 256
+    assert mm.lib().muon_packing_create((ctypes.c_int64 * 1)(0), 1, ctypes.c_void_p(at), 256, None, ctypes.byref(h)) == mm.MUON_OK
+    p = mm.MuonPacking(h.value, [0], None, None, 0)
+    q, k = torch.empty((0, 6, 64)), torch.empty((0, 2, 64))
+    assert mm.muon_attention_backward_workspace_bytes(q, k, p) == 64 * 6 * 2 * 4
+    with pytest.raises(mm.MuonError):
+        mm.muon_attention_backward_workspace_bytes(k, q, p)
+    with pytest.raises(mm.MuonError):
+        mm.muon_attention_backward_workspace_bytes(q[:, :, :12], k, p)
+    p.close()
+    with pytest.raises(RuntimeError):
+        mm.muon_attention_backward_workspace_bytes(q, k, p)

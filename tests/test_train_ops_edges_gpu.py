@@ -303,3 +303,20 @@ def test_split_keys_not_finite_logits(mm, pos, D):
         assert (host(o[:, h][torch.from_numpy(rows).cuda()], n) == 1).all(), h
         assert np.isnan(got[h, ~rows]).all() if h < 2 else np.isneginf(got[h, ~rows]).all(), h
     assert np.isneginf(got[3]).all()
+
+
+# ---------------------------------------------------------------- workspaces
+@pytest.mark.parametrize("lens", [[5], [200, 57], [1100]], ids=str)
+def test_backward_in_a_workspace_of_the_asked_size(mm, lens):
+    print(f"[case] backward of {lens} in the caller's workspace", flush=True)
+    q, k, v, do = inputs(lens, 4, 2, 64)
+    p = mm.muon_packing_create(lens)
+    o, lse = mm.muon_attention(q, k, v, p)
+    want = mm.muon_attention_backward(do, q, k, v, o, lse, p)
+    need = mm.muon_attention_backward_workspace_bytes(q, k, p)
+    room = torch.full((need + 512,), 7, dtype=torch.uint8, device="cuda")
+    got = mm.muon_attention_backward(do, q, k, v, o, lse, p, workspace=room[256:256 + need])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert (room[:256] == 7).all() and (room[256 + need:] == 7).all()
+    with pytest.raises(mm.MuonError):
+        mm.muon_attention_backward(do, q, k, v, o, lse, p, workspace=room[256:255 + need])
