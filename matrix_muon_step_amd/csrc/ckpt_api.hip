@@ -251,11 +251,8 @@ muon_status_t muon_checkpoint_grad(const muon_checkpoint_grad_t* mats, int64_t n
       b.share = plan.share;
       b.pieces = static_cast<float*>(workspace);
       bool aligned = true;
-      for (int64_t i = i0; i < i0 + count; ++i) {
-        const muon_checkpoint_grad_t& m = mats[i];
-        if (m.tokens == 0 && m.accumulate) continue;
-        if (m.tokens > 0) aligned = aligned && reinterpret_cast<uintptr_t>(m.dy) % 16 == 0 && m.dy_stride % 8 == 0;
-        GradDesc& d = b.d[b.n];
+      auto add = [&](const muon_checkpoint_grad_t& m) -> GradDesc& {
+        GradDesc& d = b.d[b.all];
         d.dy = static_cast<const unsigned char*>(m.dy);
         d.dy_stride = m.dy_stride;
         d.codes = static_cast<const unsigned char*>(m.data);
@@ -269,12 +266,27 @@ muon_status_t muon_checkpoint_grad(const muon_checkpoint_grad_t* mats, int64_t n
         d.steps = static_cast<int32_t>(tiles(m.tokens, kCkTile));
         d.g_f32 = m.g_dtype == MUON_F32;
         d.accumulate = m.accumulate;
+        return d;
+      };
+      for (int64_t i = i0; i < i0 + count; ++i) {
+        const muon_checkpoint_grad_t& m = mats[i];
+        if (m.tokens == 0) continue;
+        aligned = aligned && reinterpret_cast<uintptr_t>(m.dy) % 16 == 0 && m.dy_stride % 8 == 0;
+        const GradDesc& d = add(m);
         const int64_t t = d.mt * tiles(m.cols, kGradTile[plan.cfg]);
         b.tiles[b.n + 1] = b.tiles[b.n] + static_cast<int32_t>(t);
         b.steps[b.n + 1] = b.steps[b.n] + t * d.steps;
-        ++b.n;
+        b.all = ++b.n;
       }
-      if (b.n == 0) continue;
+      for (int64_t i = i0; i < i0 + count; ++i) {
+        const muon_checkpoint_grad_t& m = mats[i];
+        if (m.tokens > 0 || m.accumulate) continue;
+        add(m);
+        const int64_t bytes = m.outs * m.cols * (m.g_dtype == MUON_F32 ? 4 : 2);
+        b.tiles[b.all + 1] = b.tiles[b.all] + static_cast<int32_t>(tiles(bytes, kGradZeros));
+        ++b.all;
+      }
+      if (b.all == 0) continue;
       hipError_t e = launch_ckpt_grad(b, plan.cfg, aligned, s);
       if (e == hipSuccess && b.parts) e = launch_grad_join(b, s);
       if (e != hipSuccess) return hip_fail(e, "gradient launch");

@@ -65,6 +65,8 @@ struct GradDesc {
 // tiles that a share's border cuts are summed from their pieces by a second
 // launch.  Piece 2 w of the workspace is the one share w begins with when
 // that is inside a tile, piece 2 w + 1 the one it ends with otherwise.
+// Matrices without tokens stand behind the others; further work-groups store
+// their zeros, a work-group kGradZeros bytes of G (their "tiles").
 struct GradBatch {
   GradDesc d[kGradBatch];
   int32_t tiles[kGradBatch + 1];    // exclusive prefix sums of tiles
@@ -73,7 +75,9 @@ struct GradBatch {
   float* pieces;
   int32_t parts;
   int32_t n;
+  int32_t all;                      // with the matrices without tokens, n ..
 };
+constexpr int kGradZeros = 65536;
 // Square tiles of the product kernels (outs x cols).
 enum GradCfg : int32_t { kGrad256 = 0, kGrad128 = 1, kNumGradCfg = 2 };
 constexpr int kGradTile[kNumGradCfg] = {256, 128};

@@ -342,7 +342,7 @@ __device__ __forceinline__ void grad_store(const GradDesc& d, int row0, int col0
     }
 }
 
-// Steps s0 .. s1 - 1 of the tile at (m0, n0) of G; zeros where there are none.
+// Steps s0 .. s1 - 1 (one at least) of the tile at (m0, n0) of G.
 template <class C, bool ALIGNED>
 __device__ __forceinline__ void grad_tile(const GradDesc& d, int m0, int n0, int s0, int s1, LAS unsigned char* lds, int wave,
                                           int lane, f32x16_t (&acc)[C::MB][C::NB]) {
@@ -419,7 +419,7 @@ __device__ __forceinline__ void grad_tile(const GradDesc& d, int m0, int n0, int
         ld.direct(lds + fill, wave, lane);
         fill = next(fill);
       }
-  } else if (n > 0) {
+  } else {
     fetch();
     ld.blocks(lds, wave, lane);
     put(0);
@@ -493,6 +493,21 @@ __device__ __forceinline__ int grad_find(const T* __restrict__ prefix, int n, in
   return i;
 }
 
+// Zeros for bytes kGradZeros * piece on of a matrix without tokens (G is dense
+// and 16-byte aligned), by LANES lanes.  Behind all tiles, since work items in
+// between would leave some XCDs with zeros only: 2048 x 7168 in bfloat16 from
+// 777 tokens 27 us, with one such empty matrix 28, as tiles among tiles 47.
+template <int LANES>
+__device__ __forceinline__ void grad_zeros(const GradDesc& d, int64_t piece, int lane) {
+  const int64_t total = static_cast<int64_t>(d.outs) * d.cols * (d.g_f32 ? 4 : 2);
+  const int64_t end = min(total, (piece + 1) * kGradZeros);
+  for (int64_t at = piece * kGradZeros + lane * 16; at < end; at += LANES * 16) {
+    if (at + 16 <= end) gst(d.G + at, (uint4){0, 0, 0, 0});
+    else
+      for (int64_t e = at; e < end; e += 2) gst(d.G + e, static_cast<uint16_t>(0));
+  }
+}
+
 template <class C, bool ALIGNED>
 __global__ __launch_bounds__(C::NW * 64, 2) void ckpt_grad_kernel(const GradBatch b) {
   __shared__ __align__(1024) unsigned char smem[4 * C::STAGE];
@@ -501,8 +516,13 @@ __global__ __launch_bounds__(C::NW * 64, 2) void ckpt_grad_kernel(const GradBatc
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // neighbouring work items on one XCD (work-groups go to the 8 XCDs in turn)
   const int items = b.parts ? b.parts : b.tiles[b.n], per = (items + 7) / 8;
+  if (static_cast<int>(blockIdx.x) >= 8 * per) {
+    const int zero = b.tiles[b.n] + static_cast<int>(blockIdx.x) - 8 * per, mi = grad_find(b.tiles, b.all, zero);
+    grad_zeros<C::NW * 64>(b.d[mi], zero - b.tiles[mi], threadIdx.x);
+    return;
+  }
   const int item = (blockIdx.x % 8) * per + blockIdx.x / 8;
-  if (static_cast<int>(blockIdx.x) / 8 >= per || item >= items) return;
+  if (item >= items) return;
   f32x16_t acc[C::MB][C::NB];
   if (!b.parts) {
     const int mi = grad_find(b.tiles, b.n, item);
@@ -543,7 +563,7 @@ __global__ __launch_bounds__(C::NW * 64, 2) void ckpt_grad_kernel(const GradBatc
   }
 }
 
-// The tiles that a border cut (or that have no tokens): their pieces summed in
+// The tiles that a border cut: their pieces summed in
 // order, rounded once.  A work-group is one wave: 32 rows of what a wave of
 // the product kernel holds, so that even one tile's many pieces are read by
 // 32 of them.
@@ -557,12 +577,8 @@ __global__ __launch_bounds__(64) void grad_join_kernel(const GradBatch b) {
   const GradDesc d = b.d[mi];
   const int tile = item - b.tiles[mi];
   const int64_t first = b.steps[mi] + static_cast<int64_t>(tile) * d.steps, last = first + d.steps - 1;
-  int64_t w0 = 0, w1 = -1;
-  if (d.steps > 0) {
-    w0 = first / b.share;
-    w1 = last / b.share;
-    if (w0 == w1) return;  // in one piece: stored already
-  }
+  const int64_t w0 = first / b.share, w1 = last / b.share;
+  if (w0 == w1) return;  // in one piece: stored already
   f32x16_t acc[1][C::NB];
 #pragma unroll
   for (int jb = 0; jb < C::NB; ++jb) acc[0][jb] = (f32x16_t)(0.f);
@@ -600,7 +616,7 @@ hipError_t launch_ckpt_read(const CkBatch& b, hipStream_t s) {
 template <class C>
 static void launch_grad(const GradBatch& b, bool aligned, hipStream_t s) {
   const int items = b.parts ? b.parts : b.tiles[b.n];
-  const dim3 grid(static_cast<uint32_t>((items + 7) / 8 * 8));
+  const dim3 grid(static_cast<uint32_t>((items + 7) / 8 * 8 + b.tiles[b.all] - b.tiles[b.n]));
   if (aligned) hipLaunchKernelGGL((ckpt_grad_kernel<C, true>), grid, dim3(C::NW * 64), 0, s, b);
   else hipLaunchKernelGGL((ckpt_grad_kernel<C, false>), grid, dim3(C::NW * 64), 0, s, b);
 }

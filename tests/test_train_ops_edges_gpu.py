@@ -124,6 +124,19 @@ def test_only_empty_gradients(mm, outs):
     assert all((G == 0).all() for _, _, G in mats)
 
 
+@pytest.mark.parametrize("outs,cols", [(1, 1), (7, 513), (64, 512), (300, 257), (129, 1024), (1, 65536)])
+@pytest.mark.parametrize("g_type", [F32, BF16])
+def test_zeros_end_with_the_matrix(mm, outs, cols, g_type):
+    print(f"[case] zeros {outs} x {cols} {g_type}", flush=True)
+    room = torch.full((outs * cols + 64,), 7.0, dtype=g_type, device="cuda")
+    G = room[32:32 + outs * cols].view(outs, cols)
+    saved = mm.muon_checkpoint_write([torch.empty((0, cols), dtype=BF16, device="cuda")])[0]
+    some = grad_set(mm, [(40, 16, 32)], 0, g_type)
+    mm.muon_checkpoint_grad([(torch.empty((0, outs), dtype=BF16, device="cuda"), saved, G), *some])
+    assert (G == 0).all() and (room[:32] == 7).all() and (room[32 + outs * cols:] == 7).all()
+    check_grad(some[0][0], np64(mm.muon_checkpoint_read([some[0][1]], dtype=F32)[0]), some[0][2])
+
+
 # ------------------------------------------------- the end of an aligned dY
 @pytest.mark.parametrize("outs", [1, 2, 3, 5, 6, 7, 9, 14, 70, 129, 250, 259])
 @pytest.mark.parametrize("tokens", [2, 32, 45, 1000, 6000])
