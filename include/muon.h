@@ -323,7 +323,9 @@ muon_status_t muon_qk_clip(const muon_qk_clip_matrix_t* mats, int64_t n, float t
  * operators next to the Muon step: what produces the arguments of muon_step
  * and muon_qk_clip in a training step.  Attention gives each head's largest
  * logit (QK-Clip's input); a saved 8-bit activation and the upstream
- * gradient give a projection's G.
+ * gradient give a projection's G.  They were added within
+ * MUON_ABI_VERSION 7, since no earlier entry point changed: a caller that
+ * loads the library at run time looks for muon_packing_create by name.
  *
  * As for the step calls: host structures are read only during the call,
  * device memory is the caller's, everything is validated before anything is

@@ -329,10 +329,11 @@ __device__ __forceinline__ void join_acc(const LAS unsigned char* __restrict__ p
 // other's products.
 // 8192 tokens, 32 heads of 128 over 8 key heads: 522 us, 1.05 PFLOP/s, the
 // matrix cores 55% busy at the 1.9 GHz that the card holds under this load.
-// 4100 tokens in ten sequences, 25 heads of 64: 27 us, the matrix cores 29%
+// 4100 tokens in ten sequences, 25 heads of 64: 26 us, the matrix cores 29%
 // busy (with heads of 64 the exponentials and what goes with them take about
 // twice the products' cycles); the longest sequence's 21 turns, about 1 us
-// each among the others', end last.
+// each among the others', end last.  With max_logit from -infinity 33 us (see
+// atomic_max_float).
 template <int DP, bool EXACT, int SPLIT>
 __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kernel(const AttnArgs a) {
   using G = Geo<DP>;
@@ -636,7 +637,7 @@ __device__ __forceinline__ void write_msg(LAS unsigned char* __restrict__ p, con
 // The lane number, computed where it is written (two instructions) instead of
 // kept in a register: a kernel without one to spare would reload what depends
 // on it from scratch memory, and wait there for the tile loads under way too
-// (4100 tokens, 25 heads of 64: dK/dV 53 us, 44 without that).
+// (4100 tokens, 25 heads of 64: dK/dV 53 us, 46 without that).
 __device__ __forceinline__ int fresh_lane() {
   int l = 0;
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -780,8 +781,8 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
 }
 
 // The same for head dimensions up to 64 and many key tiles: 4 waves of 32 keys
-// that each take all rows of a tile and both sums, which fits 168 registers,
-// and two tiles in LDS, so that three work-groups share a unit (the pair
+// that each take all rows of a tile and both sums, in 168 registers (one value
+// that only the stores need waits in scratch memory over the loop), and two tiles in LDS, so that three work-groups share a unit (the pair
 // kernel's 83 KB leave room for one, whose start and end, about 6 us, lie
 // open).
 template <int DP, bool EXACT>

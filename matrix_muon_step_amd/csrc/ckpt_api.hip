@@ -116,6 +116,14 @@ constexpr int64_t kUnits = 256;  // compute units
 //   the work in 256-tiles cut into equal shares, one to a unit: 1.0 a step
 //     with every unit busy, the pieces (256 KB each, written and read, at 4.5
 //     TB/s) and a second launch (1600 x 6400: 404)
+// What the model chooses against each layout forced, us (256 | 128 | shares):
+//   8192 tokens, 768 x 768 34 (188 | 95 | 43 with all 256 units), three 52 (191 |
+//     94 | 52), 1600 x 1600 95 (194 | 95 | 71: it overrates the shares here)
+//   4096, 256 x 256 24 (96 | 48 | 77 with all units); 4096 x 1024 51 (100 | 51 | 57)
+//   2048, three 768 x 768 27 (53 | 27 | 35); 4096 x 4096 64 (64 | 80 | 66)
+//   512, 1600 x 1600 12 (19 | 12 | 30); 300, 768 x 768 9 (13 | 9 | 23)
+//   777, four 2048 x 7168 111 (111 | 101 | 147)
+//   16384, 768 x 2304 74 (377 | 184 | 74); 65536, 512 x 512 73 (1464 | 732 | 74)
 // Matrices without tokens (experts that none was routed to) do not count: a
 // launch of either kind stores their zeros.
 GradPlan plan_grad(const muon_checkpoint_grad_t* mats, int64_t n) {

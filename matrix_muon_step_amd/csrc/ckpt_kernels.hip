@@ -224,10 +224,12 @@ __global__ __launch_bounds__(256) void ckpt_read_kernel(const CkBatch b) {
 // registers one step ahead.  The 8-bit operand halves what the right side
 // reads of LDS and memory; its conversion (8 instructions a block and wave,
 // the exponent applied by the same instruction) runs under the products.
-// Products bound it, and beyond about 1 PFLOP/s the card's power: 1600 x 6400
-// from 16384 tokens 367 to 410 us on different cards (0.82 to 0.91 PFLOP/s;
-// bfloat16 operands through the library 475), 4096 x 4096 from 2048 tokens 67
-// us (1.03 PFLOP/s).
+// 1600 x 6400 from 16384 tokens: 363 to 410 us on different cards (0.82 to 0.92
+// PFLOP/s; bfloat16 operands through the library 475), of which the joining
+// launch takes 27; 12% of the products are padding of edge tiles (1600 is 6.25
+// x 256), and the matrix cores are busy for 53% of the product kernel's cycles
+// (58% of those of units with work).  4096 x 4096 from 2048 tokens: 64 us (1.07
+// PFLOP/s).
 template <int T_, int NWM_, int NWN_>
 struct GradGeo {
   static constexpr int T = T_, NWM = NWM_, NWN = NWN_, NW = NWM * NWN;
