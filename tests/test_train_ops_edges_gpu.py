@@ -124,6 +124,35 @@ def test_only_empty_gradients(mm, outs):
     assert all((G == 0).all() for _, _, G in mats)
 
 
+def test_many_gradients_mostly_empty_in_a_graph(mm):
+    """Several launches, some with empty matrices only, captured and replayed."""
+    print("[case] 60 gradients, 54 of them empty, in a graph", flush=True)
+    sizes = [(0, 8 + i, 40 + 3 * i) for i in range(60)]
+    for i, size in ((0, (300, 100, 64)), (20, (33, 7, 96)), (23, (5, 300, 40)), (24, (64, 64, 64)), (40, (700, 33, 130)),
+                    (47, (1, 1, 1))):
+        sizes[i] = size
+    mats = grad_set(mm, sizes, 0, F32)
+    mm.muon_checkpoint_grad(mats)
+    want = [G.clone() for _, _, G in mats]
+    for (dy, saved, G), (tokens, _, _) in zip(mats, sizes):
+        if tokens:
+            check_grad(dy, np64(mm.muon_checkpoint_read([saved], dtype=F32)[0]), G)
+        else:
+            assert (G == 0).all()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        mm.muon_checkpoint_grad(mats)
+    for _ in range(3):
+        for _, _, G in mats:
+            G.fill_(math.nan)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(G, w) for (_, _, G), w in zip(mats, want))
+    mm.muon_checkpoint_grad([m for m, size in zip(mats, sizes) if not size[0]], accumulate=True)
+    assert all(torch.equal(G, w) for (_, _, G), w in zip(mats, want))
+
+
 @pytest.mark.parametrize("outs,cols", [(1, 1), (7, 513), (64, 512), (300, 257), (129, 1024), (1, 65536)])
 @pytest.mark.parametrize("g_type", [F32, BF16])
 def test_zeros_end_with_the_matrix(mm, outs, cols, g_type):
