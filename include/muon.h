@@ -505,6 +505,41 @@ size_t muon_checkpoint_grad_workspace_bytes(const muon_checkpoint_grad_t* mats, 
 muon_status_t muon_checkpoint_grad(const muon_checkpoint_grad_t* mats, int64_t n, void* workspace,
                                    size_t workspace_bytes, void* stream);
 
+/* Global norm of a step's gradients, and clipping by it.
+ *   norm  = sqrt of the sum of g^2 over every element of every tensor
+ *   out   = g * factor, factor = max_norm / norm where norm > max_norm and
+ *           norm is finite, else 1
+ * Squares, their sums, norm and factor in float64 (no square overflows or
+ * vanishes), g * factor rounded to float32 and from there to out's type.  A
+ * norm that is NaN or infinite (a gradient holds such a value) leaves the
+ * values as they are: they reach the step unmasked, and norm tells.
+ *   g      DEVICE, count elements (0 .. MUON_MAX_GRADIENT) without gaps,
+ *          MUON_F32 or MUON_BF16, aligned to its element (16 bytes are fastest)
+ *   out    DEVICE, likewise; g itself (of one dtype) to clip in place.  Not
+ *          looked at by muon_grad_norm
+ *   norm   DEVICE, one float64.  muon_grad_norm writes it.  muon_grad_clip
+ *          reads it where norm_given != 0 (what a program made of several
+ *          calls' norms, or of several devices'), else forms and writes it
+ *   max_norm  finite, > 0
+ * Buffers that a call writes overlap nothing else of it; muon_grad_norm may
+ * be given a tensor twice.  n == 0 gives the norm 0.  Two launches (and one
+ * each for every further 96 tensors); workspace: DEVICE, 256-byte aligned,
+ * muon_grad_norm_workspace_bytes() bytes (a constant); not used, and may be
+ * NULL, where norm_given != 0. */
+#define MUON_MAX_GRADIENT 1099511627776
+typedef struct muon_gradient {
+  const void* g;
+  void* out;
+  int64_t count;
+  int32_t g_dtype;
+  int32_t out_dtype;
+} muon_gradient_t;
+size_t muon_grad_norm_workspace_bytes(void);
+muon_status_t muon_grad_norm(const muon_gradient_t* items, int64_t n, double* norm, void* workspace,
+                             size_t workspace_bytes, void* stream);
+muon_status_t muon_grad_clip(const muon_gradient_t* items, int64_t n, double max_norm, double* norm, int32_t norm_given,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Bandwidth yardstick for the HBM-bound stages (the measurement side of the
  * boundary, not part of a step): copies `bytes` from src to dst (DEVICE
  * memory, 16-byte aligned, bytes a multiple of 16, disjoint) with a plain

@@ -11,5 +11,6 @@ from .binding import (  # noqa: F401
     MuonPacking, muon_packing_create, muon_attention, muon_attention_backward,
     muon_attention_backward_workspace_bytes,
     MuonCheckpoint, muon_checkpoint_bytes, muon_checkpoint_write, muon_checkpoint_read,
-    muon_checkpoint_grad_workspace_bytes, muon_checkpoint_grad, lib, LIB_PATH,
+    muon_checkpoint_grad_workspace_bytes, muon_checkpoint_grad,
+    muon_grad_norm_workspace_bytes, muon_grad_norm, muon_grad_clip, lib, LIB_PATH,
 )

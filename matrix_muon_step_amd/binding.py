@@ -171,6 +171,16 @@ class muon_checkpoint_grad_t(ctypes.Structure):
     ]
 
 
+class muon_gradient_t(ctypes.Structure):
+    _fields_ = [
+        ("g", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("count", ctypes.c_int64),
+        ("g_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+    ]
+
+
 class MuonError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{muon_status_string(status)}: {message}")
@@ -253,6 +263,14 @@ def lib() -> ctypes.CDLL:
                 L.muon_checkpoint_grad.restype = ctypes.c_int
                 L.muon_checkpoint_grad.argtypes = [P(muon_checkpoint_grad_t), ctypes.c_int64, ctypes.c_void_p,
                                                    ctypes.c_size_t, ctypes.c_void_p]
+                L.muon_grad_norm_workspace_bytes.restype = ctypes.c_size_t
+                L.muon_grad_norm_workspace_bytes.argtypes = []
+                L.muon_grad_norm.restype = ctypes.c_int
+                L.muon_grad_norm.argtypes = [P(muon_gradient_t), ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                             ctypes.c_size_t, ctypes.c_void_p]
+                L.muon_grad_clip.restype = ctypes.c_int
+                L.muon_grad_clip.argtypes = [P(muon_gradient_t), ctypes.c_int64, ctypes.c_double, ctypes.c_void_p,
+                                             ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
                 L.muon_copy_probe.restype = ctypes.c_int
                 L.muon_copy_probe.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32,
                                               ctypes.c_void_p]
@@ -1097,3 +1115,88 @@ def muon_checkpoint_grad(matrices, accumulate=False, workspace=None, stream=None
         for _, c, _ in matrices:
             c._used_on(st)
         _check(lib().muon_checkpoint_grad(arr, len(matrices), ws_ptr, ws_len, ctypes.c_void_p(st.cuda_stream)))
+
+
+def _gradient_items(gradients, outs):
+    arr = (muon_gradient_t * max(1, len(gradients)))()
+    device = None
+    for k, g in enumerate(gradients):
+        out = g if outs is None else outs[k]
+        for name, t in (("g", g), ("out", out)):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"gradient {k}: {name} must be a contiguous GPU tensor")
+            device = _same_device(device, t, f"gradient {k}: {name}")
+        if out.shape != g.shape:
+            raise ValueError(f"gradient {k}: out is {tuple(out.shape)}, the gradient {tuple(g.shape)}")
+        arr[k] = muon_gradient_t(g.data_ptr(), out.data_ptr(), g.numel(), _dtype_code(g, f"gradient {k}"),
+                                 _dtype_code(out, f"gradient {k}: out"))
+    return arr, device
+
+
+def _norm_tensor(norm, device):
+    import torch
+
+    if not norm.is_cuda or norm.dtype != torch.float64 or norm.numel() != 1:
+        raise ValueError("norm must be a float64 GPU tensor of one element")
+    return _same_device(device, norm, "norm")
+
+
+def muon_grad_norm_workspace_bytes() -> int:
+    return int(lib().muon_grad_norm_workspace_bytes())
+
+
+def muon_grad_norm(gradients, norm=None, workspace=None, stream=None):
+    """The norm of all elements of a list of contiguous float32 or bfloat16
+    tensors, as a float64 GPU tensor of no dimensions (or written to `norm`, of
+    one element): the root of the sum of their squares, formed in float64.
+    Nothing waits for the GPU.  The caller keeps tensors of another stream
+    until the call has finished on this one."""
+    import torch
+
+    gradients = list(gradients)
+    arr, device = _gradient_items(gradients, None)
+    if norm is not None:
+        device = _norm_tensor(norm, device)
+    with _on(device, stream) as st:
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float64, device=device or st.device)
+        if workspace is None:
+            workspace = _alloc_workspace(muon_grad_norm_workspace_bytes(), norm.device)
+        ws_ptr, ws_len = _ws_args(workspace, norm.device)
+        _check(lib().muon_grad_norm(arr, len(gradients), ctypes.c_void_p(norm.data_ptr()), ws_ptr, ws_len,
+                                    ctypes.c_void_p(st.cuda_stream)))
+    return norm
+
+
+def muon_grad_clip(gradients, max_norm: float, outs=None, norm=None, workspace=None, stream=None):
+    """Scales a list of contiguous float32 or bfloat16 gradients so that the
+    norm of them all is at most max_norm; returns the norm they had (a float64
+    GPU tensor).  In place, or into `outs`, of the same shapes and either type
+    (sums of micro-batches in float32 to a step's bfloat16 G, say).  A norm that
+    is NaN or infinite leaves every value as it is.
+
+    norm: None (formed here), or the norm to go by, a float64 GPU tensor of one
+    element that is read when the stream gets there: what a program makes of
+    muon_grad_norm of several shards.  stream: as for muon_grad_norm."""
+    import torch
+
+    gradients = list(gradients)
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != len(gradients):
+            raise ValueError("outs must hold one tensor per gradient")
+    arr, device = _gradient_items(gradients, outs)
+    given = norm is not None
+    if given:
+        device = _norm_tensor(norm, device)
+    with _on(device, stream) as st:
+        if given:
+            ws_ptr, ws_len = ctypes.c_void_p(0), 0
+        else:
+            norm = torch.empty((), dtype=torch.float64, device=device or st.device)
+            if workspace is None:
+                workspace = _alloc_workspace(muon_grad_norm_workspace_bytes(), norm.device)
+            ws_ptr, ws_len = _ws_args(workspace, norm.device)
+        _check(lib().muon_grad_clip(arr, len(gradients), float(max_norm), ctypes.c_void_p(norm.data_ptr()), int(given),
+                                    ws_ptr, ws_len, ctypes.c_void_p(st.cuda_stream)))
+    return norm
