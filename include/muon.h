@@ -437,6 +437,73 @@ size_t muon_attention_backward_workspace_bytes(const muon_attention_grad_t* args
 muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_packing_t packing, void* workspace,
                                       size_t workspace_bytes, void* stream);
 
+/* Norms of queries and keys per head with rotary positions in the same pass,
+ * between the projections and attention.  Per token and head:
+ *   y_d = x_d * w_d / sqrt(mean over the head of x^2 + eps)   (norm == 0: y = x)
+ *   pair i < rotary_dim / 2 of elements (l, h): (i, rotary_dim / 2 + i), or
+ *   (2 i, 2 i + 1) where interleaved, is turned by u = position * frequency[i]:
+ *   z_l = y_l cos u - y_h sin u,  z_h = y_h cos u + y_l sin u
+ *   z_d = y_d for d >= rotary_dim
+ * Float32 throughout, z rounded to bfloat16 once.  Angles are exact modulo a
+ * turn up to 2^-65 turns a position (far positions stay as good as near ones).
+ * A token has one position per axis (time, height, width of a video, say), and
+ * each pair goes by one axis.
+ *   rotary.rotary_dim   a multiple of 8, 0 (no rotation) .. head_dim
+ *   rotary.axes         1 .. MUON_MAX_AXES
+ *   rotary.frequency    HOST, rotary_dim / 2 radians per position, each of
+ *                       magnitude <= MUON_MAX_FREQUENCY
+ *   rotary.axis         HOST, each pair's axis (0 .. axes - 1), or NULL: 0
+ *   positions  DEVICE, axes rows of position_stride (>= the packing's tokens)
+ *              integers of position_bits (32 or 64), of any sign and size; or
+ *              NULL: each token's index in its sequence, on every axis
+ *   weights    DEVICE, head_dim float32, or NULL: ones (and so without a norm)
+ *   eps        finite, >= 2^-126 (norm only)
+ *   heads, kv_heads  1 .. MUON_MAX_HEADS each; head_dim as for attention
+ * q_out may be q itself and k_out k (the same data and strides).  Rows behind
+ * the packing's last sequence are neither read nor written. */
+#define MUON_MAX_AXES 4
+#define MUON_MAX_FREQUENCY 1024
+typedef struct muon_rotary {
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t axes;
+  int32_t reserved;
+  const double* frequency;
+  const int32_t* axis;
+} muon_rotary_t;
+typedef struct muon_qk_rotate {
+  muon_heads_t q, k, q_out, k_out;
+  const float* q_weight;
+  const float* k_weight;
+  const void* positions;
+  int64_t position_stride;
+  int32_t position_bits;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t norm;
+  float eps;
+  muon_rotary_t rotary;
+} muon_qk_rotate_t;
+muon_status_t muon_qk_norm_rotate(const muon_qk_rotate_t* args, muon_packing_t packing, void* stream);
+
+/* Backward pass of muon_qk_norm_rotate: from the forward's q, k (its inputs;
+ * not looked at without a norm), weights, positions and rotary, and the
+ * gradients d_q_out and d_k_out of its outputs, with g the upstream gradient
+ * turned back and n = x / sqrt(mean x^2 + eps),
+ *   dx_d = (w_d g_d - n_d mean(w g n)) / sqrt(mean x^2 + eps)   (norm == 0: g)
+ *   dw_d = sum over tokens and heads of g_d n_d
+ * args->q_out and k_out take dq and dk (bfloat16, rounded once; they may be
+ * d_q_out and d_k_out, or q and k, themselves); d_q_weight and d_k_weight
+ * DEVICE, head_dim float32 each, written; NULL: not formed (and NULL where the
+ * weight is).  No atomics.  Workspace, where one of them is formed: DEVICE,
+ * 256-byte aligned, muon_qk_norm_rotate_backward_workspace_bytes(head_dim)
+ * bytes (0 for a head_dim that is not supported). */
+size_t muon_qk_norm_rotate_backward_workspace_bytes(int32_t head_dim);
+muon_status_t muon_qk_norm_rotate_backward(const muon_qk_rotate_t* args, const muon_heads_t* d_q_out,
+                                           const muon_heads_t* d_k_out, float* d_q_weight, float* d_k_weight,
+                                           muon_packing_t packing, void* workspace, size_t workspace_bytes, void* stream);
+
 /* 8-bit activation checkpoints: a layer's input x (tokens x cols, row-major)
  * kept from the forward to the backward pass in half the bytes of bfloat16.
  * Blocks of 32 tokens x 32 columns share the exponent e, the smallest integer

@@ -10,6 +10,7 @@ from .binding import (  # noqa: F401
     muon_profile_enable, muon_profile_read, muon_copy_probe, muon_qk_clip,
     MuonPacking, muon_packing_create, muon_attention, muon_attention_backward,
     muon_attention_backward_workspace_bytes,
+    MuonRotary, muon_qk_norm_rotate, muon_qk_norm_rotate_backward_workspace_bytes, muon_qk_norm_rotate_backward,
     MuonCheckpoint, muon_checkpoint_bytes, muon_checkpoint_write, muon_checkpoint_read,
     muon_checkpoint_grad_workspace_bytes, muon_checkpoint_grad,
     muon_grad_norm_workspace_bytes, muon_grad_norm, muon_grad_clip, lib, LIB_PATH,

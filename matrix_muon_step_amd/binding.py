@@ -29,6 +29,7 @@ MUON_BF16 = 1
 MUON_MAX_NS_STEPS = 64
 MUON_MAX_DIM = 65536
 MUON_MAX_GRAM = 16384
+MUON_MAX_AXES = 4
 MUON_COPY_PROBE_VARIANTS = 6
 MUON_STATIC_WORKSPACE_BYTES = 64 * 1024 * 1024
 STAGES = ("momentum", "norm", "prep", "gram", "poly", "bx", "update", "upload", "bx_update", "diag")
@@ -171,6 +172,33 @@ class muon_checkpoint_grad_t(ctypes.Structure):
     ]
 
 
+class muon_rotary_t(ctypes.Structure):
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("frequency", ctypes.POINTER(ctypes.c_double)),
+        ("axis", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class muon_qk_rotate_t(ctypes.Structure):
+    _fields_ = [(n, muon_heads_t) for n in ("q", "k", "q_out", "k_out")] + [
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("position_stride", ctypes.c_int64),
+        ("position_bits", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("norm", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("rotary", muon_rotary_t),
+    ]
+
+
 class muon_gradient_t(ctypes.Structure):
     _fields_ = [
         ("g", ctypes.c_void_p),
@@ -263,6 +291,14 @@ def lib() -> ctypes.CDLL:
                 L.muon_checkpoint_grad.restype = ctypes.c_int
                 L.muon_checkpoint_grad.argtypes = [P(muon_checkpoint_grad_t), ctypes.c_int64, ctypes.c_void_p,
                                                    ctypes.c_size_t, ctypes.c_void_p]
+                L.muon_qk_norm_rotate.restype = ctypes.c_int
+                L.muon_qk_norm_rotate.argtypes = [P(muon_qk_rotate_t), ctypes.c_void_p, ctypes.c_void_p]
+                L.muon_qk_norm_rotate_backward_workspace_bytes.restype = ctypes.c_size_t
+                L.muon_qk_norm_rotate_backward_workspace_bytes.argtypes = [ctypes.c_int32]
+                L.muon_qk_norm_rotate_backward.restype = ctypes.c_int
+                L.muon_qk_norm_rotate_backward.argtypes = [
+                    P(muon_qk_rotate_t), P(muon_heads_t), P(muon_heads_t), ctypes.c_void_p, ctypes.c_void_p,
+                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
                 L.muon_grad_norm_workspace_bytes.restype = ctypes.c_size_t
                 L.muon_grad_norm_workspace_bytes.argtypes = []
                 L.muon_grad_norm.restype = ctypes.c_int
@@ -942,6 +978,184 @@ def muon_attention_backward(do, q, k, v, o, lse, packing: MuonPacking, scale=Non
         _check(lib().muon_attention_backward(ctypes.byref(args), handle, ws_ptr, ws_len,
                                              ctypes.c_void_p(st.cuda_stream)))
     return outs["dq"], outs["dk"], outs["dv"]
+
+
+class MuonRotary:
+    """Rotary positions (muon_rotary_t): the first `rotary_dim` elements of a
+    head (a multiple of 8; 0: none) in pairs (i, rotary_dim / 2 + i), or
+    (2 i, 2 i + 1) where `interleaved`, pair i turned by its token's position
+    times base ** (-2 i / rotary_dim), or times frequencies[i] (radians).
+
+    Tokens with several positions (time, height, width): `sections` gives the
+    number of consecutive pairs of each axis, or `pair_axes` every pair's axis."""
+
+    def __init__(self, rotary_dim, base=10000.0, sections=None, interleaved=False, frequencies=None, pair_axes=None):
+        rotary_dim = _int64(rotary_dim, "rotary_dim")
+        if not 0 <= rotary_dim <= 128 or rotary_dim % 8:
+            raise ValueError("rotary_dim must be a multiple of 8 from 0 to 128")
+        half = rotary_dim // 2
+        if frequencies is None:
+            if not base > 0:
+                raise ValueError("base must be > 0")
+            frequencies = [float(base) ** (-i / half) for i in range(half)]
+        self.frequencies = tuple(float(f) for f in frequencies)
+        if len(self.frequencies) != half:
+            raise ValueError(f"a rotary_dim of {rotary_dim} takes {half} frequencies")
+        if sections is not None and pair_axes is not None:
+            raise ValueError("either sections or pair_axes")
+        if sections is not None:
+            sections = [_int64(n, "a section") for n in sections]
+            if min(sections, default=0) < 0 or sum(sections) != half:
+                raise ValueError(f"sections must be pair counts that sum to {half}")
+            pair_axes = [a for a, n in enumerate(sections) for _ in range(n)]
+            self.axes = len(sections)
+        elif pair_axes is not None:
+            pair_axes = [_int64(a, "a pair's axis") for a in pair_axes]
+            self.axes = max(pair_axes, default=0) + 1
+        else:
+            pair_axes, self.axes = [0] * half, 1
+        if len(pair_axes) != half or min(pair_axes, default=0) < 0:
+            raise ValueError(f"pair_axes must hold {half} axes")
+        if not 1 <= self.axes <= MUON_MAX_AXES:
+            raise ValueError(f"1 to {MUON_MAX_AXES} axes")
+        self.pair_axes = tuple(pair_axes)
+        self.rotary_dim = rotary_dim
+        self.interleaved = bool(interleaved)
+        self._t = muon_rotary_t(rotary_dim, int(self.interleaved), self.axes, 0,
+                                (ctypes.c_double * max(1, half))(*self.frequencies),
+                                (ctypes.c_int32 * max(1, half))(*pair_axes))
+
+
+_NO_ROTARY = MuonRotary(0)
+
+
+def _rotate_weight(name, w, head_dim, device):
+    import torch
+
+    if w is None:
+        return None, device
+    if not w.is_cuda or w.dtype != torch.float32 or w.shape != (head_dim,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 GPU tensor of head_dim entries")
+    return w.data_ptr(), _same_device(device, w, name)
+
+
+def _rotate_args(q, k, packing, rotary, positions, norm, q_weight, k_weight, eps, views, device):
+    """The call's muon_qk_rotate_t; q and k: tensors of the call's shapes."""
+    import torch
+
+    rotary = _NO_ROTARY if rotary is None else rotary
+    rows, heads, head_dim = q.shape
+    if k.shape[2] != head_dim:
+        raise ValueError("q and k must have one head_dim")
+    if rows < packing.tokens:
+        raise ValueError(f"q has {rows} rows, the packing {packing.tokens} tokens")
+    qw, device = _rotate_weight("q_weight", q_weight, head_dim, device)
+    kw, device = _rotate_weight("k_weight", k_weight, head_dim, device)
+    at, stride, bits = None, 0, 0
+    if positions is not None:
+        p = positions
+        if not p.is_cuda or p.dtype not in (torch.int32, torch.int64):
+            raise ValueError("positions must be an int32 or int64 GPU tensor")
+        if p.dim() == 1:
+            p = p[None]
+        if p.dim() != 2 or p.shape[0] != rotary.axes or p.shape[1] < packing.tokens:
+            raise ValueError(f"positions must be ({rotary.axes}, tokens), or (tokens) for one axis")
+        if p.shape[1] > 1 and p.stride(1) != 1:
+            raise ValueError("positions: the last dimension must be contiguous")
+        device = _same_device(device, p, "positions")
+        at, stride, bits = p.data_ptr(), p.stride(0) if p.shape[0] > 1 else p.shape[1], 8 * p.element_size()
+    return muon_qk_rotate_t(*views, qw, kw, at, stride, bits, heads, k.shape[1], head_dim, int(bool(norm)), float(eps),
+                            rotary._t), device
+
+
+def muon_qk_norm_rotate(q, k, packing: MuonPacking, rotary: Optional[MuonRotary] = None, positions=None, norm=True,
+                        q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Queries and keys on their way into muon_attention: each head divided by
+    the root of its mean square (plus eps under the root) and multiplied by the
+    float32 weights (head_dim), unless `norm` is False, and turned by its
+    token's position, unless `rotary` is None.  Returns (q_out, k_out).
+
+    q is (rows, heads, head_dim), k (rows, kv_heads, head_dim), bfloat16, views
+    taken as they are.  positions: int32 or int64, (tokens) or (axes, tokens);
+    default: each token's index in its sequence, on every axis.  q_out may be q
+    and k_out k.  Outputs given by the caller keep what they hold in rows behind
+    the last sequence, outputs made here hold zeros there.  stream: as for
+    muon_attention."""
+    rows = q.shape[0]
+    vq, device = _heads_tensor("q", q, rows, None)
+    vk, device = _heads_tensor("k", k, rows, device)
+    views = [vq, vk, None, None]
+    for i, (name, out, like) in enumerate((("q_out", q_out, q), ("k_out", k_out, k))):
+        if out is not None:
+            views[2 + i], device = _heads_tensor(name, out, rows, device, like=like)
+    made = [v or muon_heads_t() for v in views]
+    args, device = _rotate_args(q, k, packing, rotary, positions, norm, q_weight, k_weight, eps, made, device)
+    with _on(device, stream) as st:
+        if q_out is None:
+            q_out, args.q_out = _new_heads(q, packing.tokens)
+        if k_out is None:
+            k_out, args.k_out = _new_heads(k, packing.tokens)
+        _check(lib().muon_qk_norm_rotate(ctypes.byref(args), packing._enter(device, st), ctypes.c_void_p(st.cuda_stream)))
+    return q_out, k_out
+
+
+def muon_qk_norm_rotate_backward_workspace_bytes(head_dim: int) -> int:
+    """Bytes of the workspace that muon_qk_norm_rotate_backward takes for the weights' gradients."""
+    head_dim = _int64(head_dim, "head_dim")
+    nbytes = int(lib().muon_qk_norm_rotate_backward_workspace_bytes(head_dim)) if 0 < head_dim < 1 << 31 else 0
+    if nbytes == 0:
+        raise MuonError(MUON_ERR_UNSUPPORTED, muon_last_error())
+    return nbytes
+
+
+def muon_qk_norm_rotate_backward(d_q_out, d_k_out, q, k, packing: MuonPacking, rotary: Optional[MuonRotary] = None,
+                                 positions=None, norm=True, q_weight=None, k_weight=None, eps=1e-6, dq=None, dk=None,
+                                 d_q_weight=None, d_k_weight=None, workspace=None, stream=None):
+    """Gradients (dq, dk, d_q_weight, d_k_weight) of muon_qk_norm_rotate from
+    those of its outputs and what the forward call took.  Without a norm q and k
+    are not read and may be None.  dq and dk are bfloat16 and may be d_q_out and
+    d_k_out; the weights' gradients float32, written, and None where the weight
+    is.  Rows behind the last sequence, streams: as there.  workspace: a uint8
+    GPU tensor of muon_qk_norm_rotate_backward_workspace_bytes; made for the
+    call by default."""
+    import torch
+
+    rows = d_q_out.shape[0]
+    up_q, device = _heads_tensor("d_q_out", d_q_out, rows, None)
+    up_k, device = _heads_tensor("d_k_out", d_k_out, rows, device)
+    views = [None] * 4
+    if norm:
+        if q is None or k is None:
+            raise ValueError("the gradient of a norm needs q and k")
+        views[0], device = _heads_tensor("q", q, rows, device, like=d_q_out)
+        views[1], device = _heads_tensor("k", k, rows, device, like=d_k_out)
+    for i, (name, out, like) in enumerate((("dq", dq, d_q_out), ("dk", dk, d_k_out))):
+        if out is not None:
+            views[2 + i], device = _heads_tensor(name, out, rows, device, like=like)
+    made = [v or muon_heads_t() for v in views]
+    args, device = _rotate_args(d_q_out, d_k_out, packing, rotary, positions, norm, q_weight, k_weight, eps, made, device)
+    for name, d, w in (("d_q_weight", d_q_weight, q_weight), ("d_k_weight", d_k_weight, k_weight)):
+        if d is not None and w is None:
+            raise ValueError(f"{name} without the weight")
+        device = _rotate_weight(name, d, args.head_dim, device)[1]
+    with _on(device, stream) as st:
+        if dq is None:
+            dq, args.q_out = _new_heads(d_q_out, packing.tokens)
+        if dk is None:
+            dk, args.k_out = _new_heads(d_k_out, packing.tokens)
+        if q_weight is not None and d_q_weight is None:
+            d_q_weight = torch.empty_like(q_weight)
+        if k_weight is not None and d_k_weight is None:
+            d_k_weight = torch.empty_like(k_weight)
+        sums = [None if d is None else ctypes.c_void_p(d.data_ptr()) for d in (d_q_weight, d_k_weight)]
+        if workspace is None and (sums[0] or sums[1]):
+            need = int(lib().muon_qk_norm_rotate_backward_workspace_bytes(args.head_dim))
+            workspace = _alloc_workspace(need, device)
+        ws_ptr, ws_len = _ws_args(workspace, device)
+        _check(lib().muon_qk_norm_rotate_backward(ctypes.byref(args), ctypes.byref(up_q), ctypes.byref(up_k), *sums,
+                                                  packing._enter(device, st), ws_ptr, ws_len,
+                                                  ctypes.c_void_p(st.cuda_stream)))
+    return dq, dk, d_q_weight, d_k_weight
 
 
 class MuonCheckpoint:

@@ -4,34 +4,11 @@
 #include <algorithm>
 #include <memory>
 
-#include "api_common.h"
-#include "attn_internal.h"
+#include "packing.h"
 
 using namespace muon;
 
-// A packing's host side.  The device table holds two orders of the same work
-// items: by falling number of keys (a query tile sees the keys before it) and
-// by falling number of queries (a key tile is seen by the queries after it),
-// so that the longest items start first.
-struct muon_packing_s {
-  int device;
-  int64_t tokens;
-  int64_t n_tiles;
-  const AttnTile* by_query;
-  const AttnTile* by_key;
-  uintptr_t lo, hi;  // the table's bytes
-  int64_t longest;   // tokens of the longest sequence
-};
-
 namespace {
-
-// The tensors of a call with what the checks need of them.
-struct Tensor {
-  const muon_heads_t* v;
-  int64_t heads;
-  bool writable;
-  const char* name;
-};
 
 muon_status_t count_tiles(const int64_t* lengths, int64_t n, int64_t* tokens, int64_t* tiles) {
   if (n < 0 || (n > 0 && !lengths)) return fail(MUON_ERR_INVALID_ARG, "muon: packing lengths missing or n < 0");
@@ -91,13 +68,35 @@ bool apart_modulo(const Tensor& a, const Tensor& b, int64_t m, int64_t tokens, i
   return d >= span[0] && d + span[1] <= m;
 }
 
+muon_status_t check_lse(const float* lse, int64_t stride, int64_t tokens, int64_t heads, bool writable,
+                        std::vector<Range>& out) {
+  if (tokens == 0) return MUON_OK;
+  if (!lse) return fail(MUON_ERR_INVALID_ARG, "muon: attention lse is NULL");
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(MUON_ERR_ALIGN, "muon: attention lse is not 4-byte aligned");
+  if (stride < tokens) return fail(MUON_ERR_INVALID_ARG, "muon: lse_stride is smaller than the packing's tokens");
+  if (stride > (int64_t{1} << 40)) return fail(MUON_ERR_UNSUPPORTED, "muon: lse_stride too large");
+  const uintptr_t p = reinterpret_cast<uintptr_t>(lse);
+  out.push_back({p, p + 4 * static_cast<uintptr_t>((heads - 1) * stride + tokens), writable, "lse", 0});
+  return MUON_OK;
+}
+
+int64_t row_stride(muon_packing_t p) { return round_up(std::max<int64_t>(p->tokens, 1), 64); }
+
+size_t backward_bytes(const muon_attention_grad_t* a, muon_packing_t p) {
+  return align_up(static_cast<size_t>(row_stride(p)) * a->heads * 2 * sizeof(float));
+}
+
+}  // namespace
+
+namespace muon {
+
 muon_status_t check_tensors(const std::vector<Tensor>& ts, int64_t tokens, int64_t dim,
                             const std::vector<Range>& others) {
   if (tokens == 0) return MUON_OK;  // nothing is read or written
   for (const Tensor& t : ts) {
     const muon_heads_t& v = *t.v;
     auto refuse = [&](muon_status_t st, const char* why) {
-      return fail(st, std::string("muon: attention tensor ") + t.name + why);
+      return fail(st, std::string("muon: tensor ") + t.name + why);
     };
     if (!v.data) return refuse(MUON_ERR_INVALID_ARG, " is NULL");
     if (v.token_stride < 0 || v.head_stride < 0) return refuse(MUON_ERR_INVALID_ARG, " has a negative stride");
@@ -113,12 +112,12 @@ muon_status_t check_tensors(const std::vector<Tensor>& ts, int64_t tokens, int64
     const bool tok_major = (t.heads == 1 || b >= dim) && (tokens == 1 || a >= (t.heads - 1) * b + dim);
     const bool head_major = (tokens == 1 || a >= dim) && (t.heads == 1 || b >= (tokens - 1) * a + dim);
     if (!tok_major && !head_major)
-      return fail(MUON_ERR_ALIAS, std::string("muon: attention output ") + t.name + " overlaps itself");
+      return fail(MUON_ERR_ALIAS, std::string("muon: output ") + t.name + " overlaps itself");
   }
   auto lo = [](const Tensor& t) { return reinterpret_cast<uintptr_t>(t.v->data); };
   auto hi = [&](const Tensor& t) { return lo(t) + 2 * static_cast<uintptr_t>(extent(t, tokens, dim)); };
   auto clash = [&](const char* x, const char* y) {
-    return fail(MUON_ERR_ALIAS, std::string("muon: attention ") + x + " overlaps " + y);
+    return fail(MUON_ERR_ALIAS, std::string("muon: ") + x + " overlaps " + y);
   };
   for (size_t i = 0; i < ts.size(); ++i) {
     for (size_t j = i + 1; j < ts.size(); ++j) {
@@ -139,18 +138,6 @@ muon_status_t check_tensors(const std::vector<Tensor>& ts, int64_t tokens, int64
   return MUON_OK;
 }
 
-muon_status_t check_lse(const float* lse, int64_t stride, int64_t tokens, int64_t heads, bool writable,
-                        std::vector<Range>& out) {
-  if (tokens == 0) return MUON_OK;
-  if (!lse) return fail(MUON_ERR_INVALID_ARG, "muon: attention lse is NULL");
-  if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(MUON_ERR_ALIGN, "muon: attention lse is not 4-byte aligned");
-  if (stride < tokens) return fail(MUON_ERR_INVALID_ARG, "muon: lse_stride is smaller than the packing's tokens");
-  if (stride > (int64_t{1} << 40)) return fail(MUON_ERR_UNSUPPORTED, "muon: lse_stride too large");
-  const uintptr_t p = reinterpret_cast<uintptr_t>(lse);
-  out.push_back({p, p + 4 * static_cast<uintptr_t>((heads - 1) * stride + tokens), writable, "lse", 0});
-  return MUON_OK;
-}
-
 muon_status_t check_device(muon_packing_t packing) {
   if (packing->n_tiles == 0) return MUON_OK;
   int dev = 0;
@@ -162,15 +149,7 @@ muon_status_t check_device(muon_packing_t packing) {
   return MUON_OK;
 }
 
-HeadsView view(const muon_heads_t& t) { return {static_cast<unsigned char*>(t.data), t.token_stride, t.head_stride}; }
-
-int64_t row_stride(muon_packing_t p) { return round_up(std::max<int64_t>(p->tokens, 1), 64); }
-
-size_t backward_bytes(const muon_attention_grad_t* a, muon_packing_t p) {
-  return align_up(static_cast<size_t>(row_stride(p)) * a->heads * 2 * sizeof(float));
-}
-
-}  // namespace
+}  // namespace muon
 
 extern "C" {
 

@@ -72,3 +72,153 @@ def test_clip_in_place_and_arguments():
     # a given norm is read: it may lie in no output, and needs no workspace
     assert grad_clip(gradients(), norm=BASE * 3 + 16, given=1, ws=0) == mm.MUON_ERR_ALIAS
     assert grad_clip(gradients(), norm=0, given=1, ws=0) == mm.MUON_ERR_INVALID_ARG
+
+
+# ------------------------------------------------- norms and rotations
+class packing_s(ctypes.Structure):
+    """A packing's host side, of a device that is not there: what passes every check ends at that one."""
+    _fields_ = [("device", ctypes.c_int), ("tokens", ctypes.c_int64), ("n_tiles", ctypes.c_int64),
+                ("by_query", ctypes.c_void_p), ("by_key", ctypes.c_void_p), ("lo", ctypes.c_size_t),
+                ("hi", ctypes.c_size_t), ("longest", ctypes.c_int64)]
+
+
+def packing(tokens=100, tiles=1, longest=None):
+    return packing_s(77, tokens, tiles, BASE, BASE + 64, BASE, BASE + 4096, tokens if longest is None else longest)
+
+
+PASSED = (mm.MUON_ERR_HIP, mm.MUON_ERR_INVALID_ARG)   # no GPU, or not the packing's
+
+
+def passed(status):
+    return status in PASSED and ("device" in mm.muon_last_error() or "hip" in mm.muon_last_error().lower())
+
+
+def heads_at(i, heads, dim=64):
+    return bd.muon_heads_t(BASE * (2 + i), heads * dim, dim)
+
+
+KEEP = []
+
+
+def rotate(heads=4, kv=2, dim=64, rotary=None):
+    r = rotary or mm.MuonRotary(dim)
+    KEEP.append(r)
+    return bd.muon_qk_rotate_t(heads_at(0, heads, dim), heads_at(1, kv, dim), heads_at(2, heads, dim), heads_at(3, kv, dim),
+                               BASE * 20, BASE * 21, BASE * 22, 128, 64, heads, kv, dim, 1, 1e-6, r._t)
+
+
+def call_rotate(a, p=None):
+    return mm.lib().muon_qk_norm_rotate(ctypes.byref(a), ctypes.byref(p or packing()), None)
+
+
+def call_rotate_back(a, p=None, up_q=None, up_k=None, dqw=BASE * 23, dkw=BASE * 24, ws=BASE * 30, ws_bytes=1 << 30):
+    up_q = up_q or heads_at(4, a.heads, a.head_dim)
+    up_k = up_k or heads_at(5, a.kv_heads, a.head_dim)
+    return mm.lib().muon_qk_norm_rotate_backward(ctypes.byref(a), ctypes.byref(up_q), ctypes.byref(up_k),
+                                                 ctypes.c_void_p(dqw), ctypes.c_void_p(dkw), ctypes.byref(p or packing()),
+                                                 ctypes.c_void_p(ws), ws_bytes, None)
+
+
+ROTATE = [
+    (dict(heads=0), mm.MUON_ERR_INVALID_ARG), (dict(kv_heads=-1), mm.MUON_ERR_INVALID_ARG),
+    (dict(heads=4097), mm.MUON_ERR_UNSUPPORTED), (dict(kv_heads=4097), mm.MUON_ERR_UNSUPPORTED),
+    (dict(head_dim=12), mm.MUON_ERR_UNSUPPORTED), (dict(head_dim=0), mm.MUON_ERR_UNSUPPORTED),
+    (dict(head_dim=136), mm.MUON_ERR_UNSUPPORTED), (dict(eps=0.0), mm.MUON_ERR_INVALID_ARG),
+    (dict(eps=math.nan), mm.MUON_ERR_INVALID_ARG), (dict(eps=math.inf), mm.MUON_ERR_INVALID_ARG),
+    (dict(eps=1e-39), mm.MUON_ERR_INVALID_ARG), (dict(norm=0), mm.MUON_ERR_INVALID_ARG),
+    (dict(q_weight=BASE * 20 + 2), mm.MUON_ERR_ALIGN), (dict(k_weight=BASE * 20 + 1), mm.MUON_ERR_ALIGN),
+    (dict(positions=BASE * 22 + 4), mm.MUON_ERR_ALIGN), (dict(position_bits=16), mm.MUON_ERR_INVALID_ARG),
+    (dict(position_stride=99), mm.MUON_ERR_INVALID_ARG), (dict(position_stride=1 << 41), mm.MUON_ERR_INVALID_ARG),
+    (dict(positions=BASE * 4), mm.MUON_ERR_ALIAS), (dict(q_weight=BASE * 5 + 64), mm.MUON_ERR_ALIAS),
+]
+
+
+@pytest.mark.parametrize("call", [call_rotate, call_rotate_back])
+@pytest.mark.parametrize("change,status", ROTATE, ids=str)
+def test_rotate_refuses(call, change, status):
+    a = rotate()
+    for k, v in change.items():
+        setattr(a, k, v)
+    assert call(a) == status and mm.muon_last_error()
+
+
+def test_rotate_passes_on():
+    for call in (call_rotate, call_rotate_back):
+        assert passed(call(rotate()))
+        a = rotate()
+        a.q_out, a.k_out = a.q, a.k                     # over the inputs
+        assert passed(call(a))
+        a = rotate()
+        a.k_weight = a.q_weight                         # one weight for both
+        assert passed(call(a))
+        a = rotate(kv=3)                                # queries and keys need not be grouped
+        assert passed(call(a))
+    a = rotate()
+    assert passed(call_rotate_back(a, up_q=a.q_out, up_k=a.k_out))
+    a.norm, a.q_weight, a.k_weight, a.q.data, a.k.data = 0, 0, 0, 0, 0
+    assert passed(call_rotate_back(a, dqw=0, dkw=0, ws=0, ws_bytes=0))
+    assert call_rotate(a) == mm.MUON_ERR_INVALID_ARG    # the forward pass reads them
+
+
+@pytest.mark.parametrize("name", ["q", "k", "q_out", "k_out"])
+def test_rotate_refuses_views(name):
+    for call in (call_rotate, call_rotate_back):
+        for field, value, status in (("data", 0, mm.MUON_ERR_INVALID_ARG), ("data", BASE * 9 + 8, mm.MUON_ERR_ALIGN),
+                                     ("token_stride", 132, mm.MUON_ERR_ALIGN), ("token_stride", -64, mm.MUON_ERR_INVALID_ARG),
+                                     ("head_stride", 1 << 50, mm.MUON_ERR_UNSUPPORTED),
+                                     ("token_stride", 1 << 23, mm.MUON_ERR_UNSUPPORTED)):
+            a = rotate()
+            setattr(getattr(a, name), field, value)
+            assert call(a) == status, (field, value)
+    # an output that overlaps an input it is not, by one row, or another output
+    a = rotate()
+    a.q_out.data = a.q.data + 2 * a.q.token_stride
+    assert call_rotate(a) == mm.MUON_ERR_ALIAS and call_rotate_back(a) == mm.MUON_ERR_ALIAS
+    a = rotate()
+    a.k_out.data = a.q_out.data
+    assert call_rotate(a) == mm.MUON_ERR_ALIAS and call_rotate_back(a) == mm.MUON_ERR_ALIAS
+    a = rotate()
+    a.q_out.head_stride = 32                            # and itself
+    assert call_rotate(a) == mm.MUON_ERR_ALIAS
+
+
+def test_rotate_refuses_rotary():
+    for field, value, status in (("rotary_dim", 72, mm.MUON_ERR_UNSUPPORTED), ("rotary_dim", -8, mm.MUON_ERR_UNSUPPORTED),
+                                 ("rotary_dim", 12, mm.MUON_ERR_UNSUPPORTED), ("axes", 0, mm.MUON_ERR_INVALID_ARG),
+                                 ("axes", 5, mm.MUON_ERR_INVALID_ARG), ("frequency", None, mm.MUON_ERR_INVALID_ARG)):
+        a = rotate()
+        setattr(a.rotary, field, value)
+        assert call_rotate(a) == status and call_rotate_back(a) == status, field
+    a = rotate(rotary=mm.MuonRotary(64, sections=[16, 16]))
+    a.rotary.axes = 1                                   # a pair's axis that is not there
+    assert call_rotate(a) == mm.MUON_ERR_INVALID_ARG
+    a = rotate(rotary=mm.MuonRotary(64, frequencies=[1.0] * 31 + [2000.0]))
+    assert call_rotate(a) == mm.MUON_ERR_INVALID_ARG
+    a = rotate()
+    a.rotary.axis = None                                # all of the first
+    assert passed(call_rotate(a))
+
+
+def test_rotate_backward_arguments():
+    L = mm.lib()
+    need = mm.muon_qk_norm_rotate_backward_workspace_bytes(64)
+    assert call_rotate_back(rotate(), ws=0) == mm.MUON_ERR_WORKSPACE
+    assert call_rotate_back(rotate(), ws_bytes=need - 1) == mm.MUON_ERR_WORKSPACE
+    assert call_rotate_back(rotate(), ws=BASE * 30 + 64) == mm.MUON_ERR_WORKSPACE
+    assert call_rotate_back(rotate(), ws=BASE * 4) == mm.MUON_ERR_ALIAS
+    assert call_rotate_back(rotate(), dqw=BASE * 20) == mm.MUON_ERR_ALIAS
+    assert call_rotate_back(rotate(), dqw=BASE * 24 + 4) == mm.MUON_ERR_ALIAS
+    assert call_rotate_back(rotate(), dqw=BASE * 23 + 2) == mm.MUON_ERR_ALIGN
+    assert passed(call_rotate_back(rotate(), dqw=0, dkw=0, ws=0, ws_bytes=0))
+    assert passed(call_rotate_back(rotate(), dqw=0))
+    a = rotate()
+    a.k_weight = 0
+    assert call_rotate_back(a) == mm.MUON_ERR_INVALID_ARG and passed(call_rotate_back(a, dkw=0))
+    up = heads_at(4, 4)
+    up.data = rotate().k_out.data
+    assert call_rotate_back(rotate(), up_q=up) == mm.MUON_ERR_ALIAS
+    for args in ((None, ctypes.byref(up), ctypes.byref(up)), (ctypes.byref(rotate()), None, ctypes.byref(up)),
+                 (ctypes.byref(rotate()), ctypes.byref(up), None)):
+        assert L.muon_qk_norm_rotate_backward(*args, None, None, ctypes.byref(packing()), None, 0, None) == mm.MUON_ERR_INVALID_ARG
+    assert L.muon_qk_norm_rotate(None, ctypes.byref(packing()), None) == mm.MUON_ERR_INVALID_ARG
+    assert L.muon_qk_norm_rotate(ctypes.byref(rotate()), None, None) == mm.MUON_ERR_INVALID_ARG
