@@ -437,6 +437,26 @@ size_t muon_attention_backward_workspace_bytes(const muon_attention_grad_t* args
 muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_packing_t packing, void* workspace,
                                       size_t workspace_bytes, void* stream);
 
+/* Attention with a sliding window and first tokens that stay visible: as
+ * muon_attention, but row i of a sequence sees its row j <= i where i - j <
+ * window, or j < sinks.
+ *   window  >= 1: the row itself and the window - 1 before it.  A window that
+ *           hides no key of the packing gives muon_attention's bits
+ *   sinks   0 .. MUON_MAX_SINKS first rows of each sequence
+ * max_logit is over visible pairs.  A NaN or infinity in a sequence may reach
+ * rows of it that do not see it, as there.  The backward workspace
+ * holds, beside muon_attention_backward's, 8 * head_dim * kv_heads * sinks
+ * bytes for every 1024 rows of a sequence, times 4 for up to 32 sinks and 2 for
+ * up to 64. */
+#define MUON_MAX_SINKS 128
+muon_status_t muon_window_attention(const muon_attention_t* args, int64_t window, int64_t sinks, muon_packing_t packing,
+                                    void* stream);
+size_t muon_window_attention_backward_workspace_bytes(const muon_attention_grad_t* args, int64_t window, int64_t sinks,
+                                                      muon_packing_t packing);
+muon_status_t muon_window_attention_backward(const muon_attention_grad_t* args, int64_t window, int64_t sinks,
+                                             muon_packing_t packing, void* workspace, size_t workspace_bytes,
+                                             void* stream);
+
 /* Norms of queries and keys per head with rotary positions in the same pass,
  * between the projections and attention.  Per token and head:
  *   y_d = x_d * w_d / sqrt(mean over the head of x^2 + eps)   (norm == 0: y = x)

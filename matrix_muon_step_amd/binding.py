@@ -30,6 +30,7 @@ MUON_MAX_NS_STEPS = 64
 MUON_MAX_DIM = 65536
 MUON_MAX_GRAM = 16384
 MUON_MAX_AXES = 4
+MUON_MAX_SINKS = 128
 MUON_COPY_PROBE_VARIANTS = 6
 MUON_STATIC_WORKSPACE_BYTES = 64 * 1024 * 1024
 STAGES = ("momentum", "norm", "prep", "gram", "poly", "bx", "update", "upload", "bx_update", "diag")
@@ -291,6 +292,16 @@ def lib() -> ctypes.CDLL:
                 L.muon_checkpoint_grad.restype = ctypes.c_int
                 L.muon_checkpoint_grad.argtypes = [P(muon_checkpoint_grad_t), ctypes.c_int64, ctypes.c_void_p,
                                                    ctypes.c_size_t, ctypes.c_void_p]
+                L.muon_window_attention.restype = ctypes.c_int
+                L.muon_window_attention.argtypes = [P(muon_attention_t), ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                                    ctypes.c_void_p]
+                L.muon_window_attention_backward_workspace_bytes.restype = ctypes.c_size_t
+                L.muon_window_attention_backward_workspace_bytes.argtypes = [P(muon_attention_grad_t), ctypes.c_int64,
+                                                                             ctypes.c_int64, ctypes.c_void_p]
+                L.muon_window_attention_backward.restype = ctypes.c_int
+                L.muon_window_attention_backward.argtypes = [
+                    P(muon_attention_grad_t), ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                    ctypes.c_size_t, ctypes.c_void_p]
                 L.muon_qk_norm_rotate.restype = ctypes.c_int
                 L.muon_qk_norm_rotate.argtypes = [P(muon_qk_rotate_t), ctypes.c_void_p, ctypes.c_void_p]
                 L.muon_qk_norm_rotate_backward_workspace_bytes.restype = ctypes.c_size_t
@@ -882,8 +893,22 @@ def _new_heads(like, tokens):
     return t, muon_heads_t(t.data_ptr(), heads * dim, dim)
 
 
-def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, max_logit=None, stream=None):
+def _window(window, sinks):
+    """The window's arguments of the library's calls; none without a window (then the first tokens are seen anyway)."""
+    sinks = _int64(sinks, "sinks")
+    if window is None:
+        if not 0 <= sinks <= MUON_MAX_SINKS:
+            raise ValueError(f"sinks must be 0 to {MUON_MAX_SINKS}")
+        return ()
+    return _int64(window, "window"), sinks
+
+
+def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, max_logit=None, stream=None, window=None,
+                   sinks=0):
     """Causal self-attention of packed sequences; returns (o, lse).
+
+    window: None, or how many rows a row sees, itself and those before it;
+    sinks: how many first rows of its sequence it sees besides (0 to 128).
 
     q is (rows, heads, head_dim), k and v (rows, kv_heads, head_dim), bfloat16,
     rows >= packing.tokens; views into a fused projection output are taken as
@@ -901,6 +926,7 @@ def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, 
     the call has finished on this one (the packing keeps its own memory)."""
     import torch
 
+    seen = _window(window, sinks)
     rows = _attention_rows(q, k, v, packing)
     dq, device = _heads_tensor("q", q, rows, None)
     dk, device = _heads_tensor("k", k, rows, device)
@@ -927,30 +953,38 @@ def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, 
         args = muon_attention_t(dq, dk, dv, do, lse.data_ptr(), lse.stride(0) if heads > 1 else rows,
                                 max_logit.data_ptr() if max_logit is not None else None, logit_heads, heads, kv_heads,
                                 head_dim, float(head_dim ** -0.5 if scale is None else scale))
-        _check(lib().muon_attention(ctypes.byref(args), packing._enter(device, st), ctypes.c_void_p(st.cuda_stream)))
+        call = lib().muon_window_attention if seen else lib().muon_attention
+        _check(call(ctypes.byref(args), *seen, packing._enter(device, st), ctypes.c_void_p(st.cuda_stream)))
     return o, lse
 
 
-def muon_attention_backward_workspace_bytes(q, k, packing: MuonPacking) -> int:
-    """Bytes of the workspace that muon_attention_backward takes for such q and k."""
-    packing._open()
-    args = muon_attention_grad_t(heads=q.shape[1], kv_heads=k.shape[1], head_dim=q.shape[2], scale=1.0)
-    nbytes = int(lib().muon_attention_backward_workspace_bytes(ctypes.byref(args), ctypes.c_void_p(packing._h)))
+def _backward_bytes(args, seen, handle):
+    need = lib().muon_window_attention_backward_workspace_bytes if seen else lib().muon_attention_backward_workspace_bytes
+    nbytes = int(need(ctypes.byref(args), *seen, handle))
     if nbytes == 0:
         raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error())
     return nbytes
 
 
+def muon_attention_backward_workspace_bytes(q, k, packing: MuonPacking, window=None, sinks=0) -> int:
+    """Bytes of the workspace that muon_attention_backward takes for such q and k."""
+    packing._open()
+    args = muon_attention_grad_t(heads=q.shape[1], kv_heads=k.shape[1], head_dim=q.shape[2], scale=1.0)
+    return _backward_bytes(args, _window(window, sinks), ctypes.c_void_p(packing._h))
+
+
 def muon_attention_backward(do, q, k, v, o, lse, packing: MuonPacking, scale=None, dq=None, dk=None, dv=None,
-                            workspace=None, stream=None):
+                            workspace=None, stream=None, window=None, sinks=0):
     """Gradients (dq, dk, dv) of muon_attention, bfloat16, from the upstream
-    gradient `do` and what the forward call took and returned.  As there,
+    gradient `do` and what the forward call took and returned (`window` and
+    `sinks` as there).  As there,
     rows behind the last sequence stay as they are in outputs given by the
     caller and are zero in outputs made here, and the caller keeps tensors of
     another stream until the call has finished.  workspace: a uint8 GPU tensor
     of muon_attention_backward_workspace_bytes; made for the call by default."""
     import torch
 
+    seen = _window(window, sinks)
     rows = _attention_rows(q, k, v, packing)
     device, views = None, {}
     for name, t, like in (("q", q, None), ("k", k, None), ("v", v, None), ("o", o, q), ("do", do, q)):
@@ -969,14 +1003,11 @@ def muon_attention_backward(do, q, k, v, o, lse, packing: MuonPacking, scale=Non
                                      lse.stride(0) if heads > 1 else rows, views["dq"], views["dk"], views["dv"], heads,
                                      kv_heads, head_dim, float(head_dim ** -0.5 if scale is None else scale))
         handle = packing._enter(device, st)
-        need = int(lib().muon_attention_backward_workspace_bytes(ctypes.byref(args), handle))
-        if need == 0:
-            raise MuonError(MUON_ERR_INVALID_ARG, muon_last_error())
         if workspace is None:
-            workspace = _alloc_workspace(need, device)
+            workspace = _alloc_workspace(_backward_bytes(args, seen, handle), device)
         ws_ptr, ws_len = _ws_args(workspace, device)
-        _check(lib().muon_attention_backward(ctypes.byref(args), handle, ws_ptr, ws_len,
-                                             ctypes.c_void_p(st.cuda_stream)))
+        call = lib().muon_window_attention_backward if seen else lib().muon_attention_backward
+        _check(call(ctypes.byref(args), *seen, handle, ws_ptr, ws_len, ctypes.c_void_p(st.cuda_stream)))
     return outs["dq"], outs["dk"], outs["dv"]
 
 

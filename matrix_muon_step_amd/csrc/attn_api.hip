@@ -80,10 +80,52 @@ muon_status_t check_lse(const float* lse, int64_t stride, int64_t tokens, int64_
   return MUON_OK;
 }
 
+// What rows see: every key before them, or a window and the first tokens.
+struct Window {
+  int64_t window;  // 0: none
+  int64_t sinks;
+};
+
+muon_status_t check_window(const Window* w) {
+  if (!w) return MUON_OK;
+  if (w->window < 1) return fail(MUON_ERR_INVALID_ARG, "muon: window must be >= 1");
+  if (w->sinks < 0) return fail(MUON_ERR_INVALID_ARG, "muon: sinks must be >= 0");
+  if (w->sinks > MUON_MAX_SINKS) return fail(MUON_ERR_UNSUPPORTED, "muon: more than MUON_MAX_SINKS sinks");
+  return MUON_OK;
+}
+
+// Whether the window hides any key of the packing's sequences.
+bool hides(const Window* w, muon_packing_t p) { return w && w->window < p->longest; }
+
+// Sets what the kernels need of the window; false where the causal kernels serve.
+bool set_window(AttnArgs& a, const Window* w, muon_packing_t p) {
+  a.longest = static_cast<int32_t>(p->longest);
+  if (!hides(w, p)) return false;
+  a.window = static_cast<int32_t>(w->window);
+  a.sinks = static_cast<int32_t>(w->sinks);
+  a.longest = static_cast<int32_t>(std::min<int64_t>(p->longest, w->window + w->sinks + kAttnRows));
+  return true;
+}
+
 int64_t row_stride(muon_packing_t p) { return round_up(std::max<int64_t>(p->tokens, 1), 64); }
 
-size_t backward_bytes(const muon_attention_grad_t* a, muon_packing_t p) {
-  return align_up(static_cast<size_t>(row_stride(p)) * a->heads * 2 * sizeof(float));
+// Sums for the first tokens that one chunk and key head leaves: the waves that
+// share a 32-key block of them.
+int32_t far_parts(const Window* w, muon_packing_t p) {
+  if (!hides(w, p) || w->sinks == 0) return 0;
+  return w->sinks <= 32 ? 4 : w->sinks <= 64 ? 2 : 1;
+}
+
+size_t row_bytes(int32_t heads, muon_packing_t p) {
+  return align_up(static_cast<size_t>(row_stride(p)) * heads * 2 * sizeof(float));
+}
+
+size_t backward_bytes(const muon_attention_grad_t& g, const Window* w, muon_packing_t p) {
+  size_t bytes = row_bytes(g.heads, p);
+  if (const int32_t parts = far_parts(w, p))
+    bytes += align_up(static_cast<size_t>(p->chunks) * g.kv_heads * parts * 2 * static_cast<size_t>(w->sinks) * g.head_dim *
+                      sizeof(float));
+  return bytes;
 }
 
 }  // namespace
@@ -151,6 +193,125 @@ muon_status_t check_device(muon_packing_t packing) {
 
 }  // namespace muon
 
+namespace {
+
+muon_status_t attention(const muon_attention_t* args, const Window* w, muon_packing_t packing, void* stream) {
+  if (!args) return fail(MUON_ERR_INVALID_ARG, "muon: args is NULL");
+  const muon_attention_t& g = *args;
+  muon_status_t st = check_shape(g.heads, g.kv_heads, g.head_dim, g.scale, packing);
+  if (st != MUON_OK) return st;
+  st = check_window(w);
+  if (st != MUON_OK) return st;
+  std::vector<Range> others;
+  st = check_lse(g.lse, g.lse_stride, packing->tokens, g.heads, true, others);
+  if (st != MUON_OK) return st;
+  if (g.max_logit) {
+    if (reinterpret_cast<uintptr_t>(g.max_logit) & 3u)
+      return fail(MUON_ERR_ALIGN, "muon: attention max_logit is not 4-byte aligned");
+    if (g.logit_heads != g.heads && g.logit_heads != g.kv_heads)
+      return fail(MUON_ERR_INVALID_ARG, "muon: logit_heads must be heads or kv_heads");
+    const uintptr_t p = reinterpret_cast<uintptr_t>(g.max_logit);
+    others.push_back({p, p + 4 * static_cast<uintptr_t>(g.logit_heads), true, "max_logit", 0});
+  }
+  others.push_back({packing->lo, packing->hi, false, "the packing's table", 0});
+  st = check_tensors({{&g.q, g.heads, false, "q"}, {&g.k, g.kv_heads, false, "k"}, {&g.v, g.kv_heads, false, "v"},
+                      {&g.o, g.heads, true, "o"}},
+                     packing->tokens, g.head_dim, others);
+  if (st != MUON_OK) return st;
+  st = check_device(packing);
+  if (st != MUON_OK || packing->n_tiles == 0) return st;
+  AttnArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = view(g.q);
+  a.k = view(g.k);
+  a.v = view(g.v);
+  a.o = view(g.o);
+  a.lse = g.lse;
+  a.lse_stride = g.lse_stride;
+  a.max_logit = g.max_logit;
+  a.logit_group = g.max_logit ? g.heads / g.logit_heads : 1;
+  a.heads = g.heads;
+  a.kv_heads = g.kv_heads;
+  a.head_dim = g.head_dim;
+  a.scale = g.scale;
+  a.by_query = packing->by_query;
+  a.by_key = packing->by_key;
+  a.n_tiles = static_cast<int32_t>(packing->n_tiles);
+  const bool windowed = set_window(a, w, packing);
+  const hipError_t e = (windowed ? launch_window_attention : launch_attention)(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MUON_OK : hip_fail(e, "attention launch");
+}
+
+size_t attention_backward_bytes(const muon_attention_grad_t* args, const Window* w, muon_packing_t packing) {
+  size_t bytes = 0;
+  guarded([&] {
+    if (!args) return fail(MUON_ERR_INVALID_ARG, "muon: args is NULL");
+    muon_status_t st = check_shape(args->heads, args->kv_heads, args->head_dim, args->scale, packing);
+    if (st == MUON_OK) st = check_window(w);
+    if (st == MUON_OK) bytes = backward_bytes(*args, w, packing);
+    return st;
+  });
+  return bytes;
+}
+
+muon_status_t attention_backward(const muon_attention_grad_t* args, const Window* w, muon_packing_t packing,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!args) return fail(MUON_ERR_INVALID_ARG, "muon: args is NULL");
+  const muon_attention_grad_t& g = *args;
+  muon_status_t st = check_shape(g.heads, g.kv_heads, g.head_dim, g.scale, packing);
+  if (st != MUON_OK) return st;
+  st = check_window(w);
+  if (st != MUON_OK) return st;
+  const size_t need = backward_bytes(g, w, packing);
+  if (!workspace || workspace_bytes < need)
+    return fail(MUON_ERR_WORKSPACE, "muon: the attention backward needs " + std::to_string(need) +
+                                        " bytes of workspace");
+  const uintptr_t ws = reinterpret_cast<uintptr_t>(workspace);
+  if (ws % kAlign) return fail(MUON_ERR_WORKSPACE, "muon: workspace must be 256-byte aligned");
+  std::vector<Range> others;
+  st = check_lse(g.lse, g.lse_stride, packing->tokens, g.heads, false, others);
+  if (st != MUON_OK) return st;
+  others.push_back({ws, ws + need, true, "the workspace", 0});
+  others.push_back({packing->lo, packing->hi, false, "the packing's table", 0});
+  st = check_tensors({{&g.q, g.heads, false, "q"}, {&g.k, g.kv_heads, false, "k"}, {&g.v, g.kv_heads, false, "v"},
+                      {&g.o, g.heads, false, "o"}, {&g.d_o, g.heads, false, "d_o"}, {&g.dq, g.heads, true, "dq"},
+                      {&g.dk, g.kv_heads, true, "dk"}, {&g.dv, g.kv_heads, true, "dv"}},
+                     packing->tokens, g.head_dim, others);
+  if (st != MUON_OK) return st;
+  st = check_device(packing);
+  if (st != MUON_OK || packing->n_tiles == 0) return st;
+  AttnArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = view(g.q);
+  a.k = view(g.k);
+  a.v = view(g.v);
+  a.o = view(g.o);
+  a.d_o = view(g.d_o);
+  a.dq = view(g.dq);
+  a.dk = view(g.dk);
+  a.dv = view(g.dv);
+  a.lse = const_cast<float*>(g.lse);  // read only by the backward kernels
+  a.lse_stride = g.lse_stride;
+  a.row_stride = row_stride(packing);
+  a.row_lse2 = static_cast<float*>(workspace);
+  a.row_delta = a.row_lse2 + a.row_stride * g.heads;
+  a.heads = g.heads;
+  a.kv_heads = g.kv_heads;
+  a.head_dim = g.head_dim;
+  a.scale = g.scale;
+  a.by_query = packing->by_query;
+  a.by_key = packing->by_key;
+  a.n_tiles = static_cast<int32_t>(packing->n_tiles);
+  const bool windowed = set_window(a, w, packing);
+  a.far_parts = far_parts(w, packing);
+  a.far = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + row_bytes(g.heads, packing));
+  const hipError_t e =
+      (windowed ? launch_window_attention_backward : launch_attention_backward)(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MUON_OK : hip_fail(e, "attention backward launch");
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t muon_packing_bytes(const int64_t* lengths, int64_t n) {
@@ -178,11 +339,13 @@ muon_status_t muon_packing_create(const int64_t* lengths, int64_t n, void* table
     if (reinterpret_cast<uintptr_t>(table) % kAlign)
       return fail(MUON_ERR_WORKSPACE, "muon: the packing table must be 256-byte aligned");
     std::vector<AttnTile> all(2 * tiles);
-    int64_t k = 0, row0 = 0;
+    int64_t k = 0, row0 = 0, chunks = 0;
     for (int64_t i = 0; i < n; ++i) {
       for (int64_t first = 0; first < lengths[i]; first += kAttnRows)
-        all[k++] = {static_cast<int32_t>(row0), static_cast<int32_t>(lengths[i]), static_cast<int32_t>(first), 0};
+        all[k++] = {static_cast<int32_t>(row0), static_cast<int32_t>(lengths[i]), static_cast<int32_t>(first),
+                    static_cast<int32_t>(chunks)};
       row0 += lengths[i];
+      chunks += (lengths[i] + kFarRows - 1) / kFarRows;
     }
     std::copy(all.begin(), all.begin() + tiles, all.begin() + tiles);
     std::stable_sort(all.begin(), all.begin() + tiles,
@@ -210,6 +373,7 @@ muon_status_t muon_packing_create(const int64_t* lengths, int64_t n, void* table
     p->by_key = p->by_query + tiles;
     p->lo = reinterpret_cast<uintptr_t>(table);
     p->hi = p->lo + need;
+    p->chunks = chunks;
     p->longest = n > 0 ? *std::max_element(lengths, lengths + n) : 0;
     *out = p.release();
     return MUON_OK;
@@ -223,114 +387,35 @@ muon_status_t muon_packing_destroy(muon_packing_t packing) {
 }
 
 muon_status_t muon_attention(const muon_attention_t* args, muon_packing_t packing, void* stream) {
-  return guarded([&] {
-    if (!args) return fail(MUON_ERR_INVALID_ARG, "muon: args is NULL");
-    const muon_attention_t& g = *args;
-    muon_status_t st = check_shape(g.heads, g.kv_heads, g.head_dim, g.scale, packing);
-    if (st != MUON_OK) return st;
-    std::vector<Range> others;
-    st = check_lse(g.lse, g.lse_stride, packing->tokens, g.heads, true, others);
-    if (st != MUON_OK) return st;
-    if (g.max_logit) {
-      if (reinterpret_cast<uintptr_t>(g.max_logit) & 3u)
-        return fail(MUON_ERR_ALIGN, "muon: attention max_logit is not 4-byte aligned");
-      if (g.logit_heads != g.heads && g.logit_heads != g.kv_heads)
-        return fail(MUON_ERR_INVALID_ARG, "muon: logit_heads must be heads or kv_heads");
-      const uintptr_t p = reinterpret_cast<uintptr_t>(g.max_logit);
-      others.push_back({p, p + 4 * static_cast<uintptr_t>(g.logit_heads), true, "max_logit", 0});
-    }
-    others.push_back({packing->lo, packing->hi, false, "the packing's table", 0});
-    st = check_tensors({{&g.q, g.heads, false, "q"}, {&g.k, g.kv_heads, false, "k"}, {&g.v, g.kv_heads, false, "v"},
-                        {&g.o, g.heads, true, "o"}},
-                       packing->tokens, g.head_dim, others);
-    if (st != MUON_OK) return st;
-    st = check_device(packing);
-    if (st != MUON_OK || packing->n_tiles == 0) return st;
-    AttnArgs a;
-    memset(&a, 0, sizeof(a));
-    a.q = view(g.q);
-    a.k = view(g.k);
-    a.v = view(g.v);
-    a.o = view(g.o);
-    a.lse = g.lse;
-    a.lse_stride = g.lse_stride;
-    a.max_logit = g.max_logit;
-    a.logit_group = g.max_logit ? g.heads / g.logit_heads : 1;
-    a.heads = g.heads;
-    a.kv_heads = g.kv_heads;
-    a.head_dim = g.head_dim;
-    a.scale = g.scale;
-    a.by_query = packing->by_query;
-    a.by_key = packing->by_key;
-    a.n_tiles = static_cast<int32_t>(packing->n_tiles);
-    a.longest = static_cast<int32_t>(packing->longest);
-    const hipError_t e = launch_attention(a, static_cast<hipStream_t>(stream));
-    return e == hipSuccess ? MUON_OK : hip_fail(e, "attention launch");
-  });
+  return guarded([&] { return attention(args, nullptr, packing, stream); });
+}
+
+muon_status_t muon_window_attention(const muon_attention_t* args, int64_t window, int64_t sinks, muon_packing_t packing,
+                                    void* stream) {
+  const Window w = {window, sinks};
+  return guarded([&] { return attention(args, &w, packing, stream); });
 }
 
 size_t muon_attention_backward_workspace_bytes(const muon_attention_grad_t* args, muon_packing_t packing) {
-  size_t bytes = 0;
-  guarded([&] {
-    if (!args) return fail(MUON_ERR_INVALID_ARG, "muon: args is NULL");
-    const muon_status_t st = check_shape(args->heads, args->kv_heads, args->head_dim, args->scale, packing);
-    if (st == MUON_OK) bytes = backward_bytes(args, packing);
-    return st;
-  });
-  return bytes;
+  return attention_backward_bytes(args, nullptr, packing);
+}
+
+size_t muon_window_attention_backward_workspace_bytes(const muon_attention_grad_t* args, int64_t window, int64_t sinks,
+                                                      muon_packing_t packing) {
+  const Window w = {window, sinks};
+  return attention_backward_bytes(args, &w, packing);
 }
 
 muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_packing_t packing, void* workspace,
                                       size_t workspace_bytes, void* stream) {
-  return guarded([&] {
-    if (!args) return fail(MUON_ERR_INVALID_ARG, "muon: args is NULL");
-    const muon_attention_grad_t& g = *args;
-    muon_status_t st = check_shape(g.heads, g.kv_heads, g.head_dim, g.scale, packing);
-    if (st != MUON_OK) return st;
-    const size_t need = backward_bytes(args, packing);
-    if (!workspace || workspace_bytes < need)
-      return fail(MUON_ERR_WORKSPACE, "muon: the attention backward needs " + std::to_string(need) +
-                                          " bytes of workspace");
-    const uintptr_t ws = reinterpret_cast<uintptr_t>(workspace);
-    if (ws % kAlign) return fail(MUON_ERR_WORKSPACE, "muon: workspace must be 256-byte aligned");
-    std::vector<Range> others;
-    st = check_lse(g.lse, g.lse_stride, packing->tokens, g.heads, false, others);
-    if (st != MUON_OK) return st;
-    others.push_back({ws, ws + need, true, "the workspace", 0});
-    others.push_back({packing->lo, packing->hi, false, "the packing's table", 0});
-    st = check_tensors({{&g.q, g.heads, false, "q"}, {&g.k, g.kv_heads, false, "k"}, {&g.v, g.kv_heads, false, "v"},
-                        {&g.o, g.heads, false, "o"}, {&g.d_o, g.heads, false, "d_o"}, {&g.dq, g.heads, true, "dq"},
-                        {&g.dk, g.kv_heads, true, "dk"}, {&g.dv, g.kv_heads, true, "dv"}},
-                       packing->tokens, g.head_dim, others);
-    if (st != MUON_OK) return st;
-    st = check_device(packing);
-    if (st != MUON_OK || packing->n_tiles == 0) return st;
-    AttnArgs a;
-    memset(&a, 0, sizeof(a));
-    a.q = view(g.q);
-    a.k = view(g.k);
-    a.v = view(g.v);
-    a.o = view(g.o);
-    a.d_o = view(g.d_o);
-    a.dq = view(g.dq);
-    a.dk = view(g.dk);
-    a.dv = view(g.dv);
-    a.lse = const_cast<float*>(g.lse);  // read only by the backward kernels
-    a.lse_stride = g.lse_stride;
-    a.row_stride = row_stride(packing);
-    a.row_lse2 = static_cast<float*>(workspace);
-    a.row_delta = a.row_lse2 + a.row_stride * g.heads;
-    a.heads = g.heads;
-    a.kv_heads = g.kv_heads;
-    a.head_dim = g.head_dim;
-    a.scale = g.scale;
-    a.by_query = packing->by_query;
-    a.by_key = packing->by_key;
-    a.n_tiles = static_cast<int32_t>(packing->n_tiles);
-    a.longest = static_cast<int32_t>(packing->longest);
-    const hipError_t e = launch_attention_backward(a, static_cast<hipStream_t>(stream));
-    return e == hipSuccess ? MUON_OK : hip_fail(e, "attention backward launch");
-  });
+  return guarded([&] { return attention_backward(args, nullptr, packing, workspace, workspace_bytes, stream); });
+}
+
+muon_status_t muon_window_attention_backward(const muon_attention_grad_t* args, int64_t window, int64_t sinks,
+                                             muon_packing_t packing, void* workspace, size_t workspace_bytes,
+                                             void* stream) {
+  const Window w = {window, sinks};
+  return guarded([&] { return attention_backward(args, &w, packing, workspace, workspace_bytes, stream); });
 }
 
 }  // extern "C"

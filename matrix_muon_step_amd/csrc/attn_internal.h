@@ -12,6 +12,9 @@ constexpr int kAttnRows = 128;
 // Rows of the tiles that stream through LDS past a work item.
 constexpr int kAttnStep = 64;
 constexpr int kAttnMaxDim = 128;
+// Rows of a sequence that one work item of the first tokens' gradients sums
+// over (a multiple of kAttnRows).
+constexpr int kFarRows = 1024;
 constexpr float kAttnLog2e = 1.44269504088896340736f;
 
 // One work item of a packing: rows first .. first + min(kAttnRows, len -
@@ -20,7 +23,7 @@ struct AttnTile {
   int32_t row0;
   int32_t len;
   int32_t first;
-  int32_t pad;
+  int32_t chunk;  // kFarRows chunks of the sequences before it
 };
 
 // A (tokens, heads, head_dim) bf16 tensor: element strides of a token and a
@@ -45,10 +48,16 @@ struct AttnArgs {
   const AttnTile* by_query;    // tiles, most keys first
   const AttnTile* by_key;      // tiles, most queries first
   int32_t n_tiles;
-  int32_t longest;             // tokens of the longest sequence
+  int32_t longest;             // most keys that a row's work item visits: tokens of the longest sequence, or fewer
+  // windowed calls only
+  int32_t window, sinks;       // row i sees key j <= i where i - j < window or j < sinks
+  int32_t far_parts;           // backward: sums of a chunk's rows beyond their windows (0: there are none)
+  float* far;                  // backward workspace: those sums
 };
 
 hipError_t launch_attention(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attention_backward(const AttnArgs& a, hipStream_t s);
+hipError_t launch_window_attention(const AttnArgs& a, hipStream_t s);
+hipError_t launch_window_attention_backward(const AttnArgs& a, hipStream_t s);
 
 }  // namespace muon

@@ -1,0 +1,111 @@
+// Windowed attention: the kernels' instances (attn_kernels.h), and what rows
+// beyond their windows give the gradients of the first tokens.
+#include "attn_kernels.h"
+
+namespace muon {
+
+namespace {
+
+// The first tokens are seen by every row, so their dK and dV are sums over
+// the whole sequence, where other key tiles' are over a window's rows.  The
+// pairs (row, first token) beyond the window are summed here, a work-group for
+// kFarRows rows of a sequence and a key head, into float32 sums of their own
+// that the dK/dV kernel adds in order: no work-group walks the whole sequence,
+// and no atomics.  Rows stream past as in the dK/dV kernels.  The 4 waves
+// share out 32-key blocks of the first tokens, and what is left over, the rows:
+// with up to 32 of them each wave takes a 32-row half of every other tile, with
+// up to 64 one half of every tile.
+template <int DP, bool EXACT>
+__global__ __launch_bounds__(256, 2) void attention_far_kernel(const AttnArgs a) {
+  using G = Geo<DP>;
+  using L = DkvLds<DP>;
+  __shared__ __align__(1024) unsigned char smem[2 * L::STAGE];
+  LAS unsigned char* lds = (LAS unsigned char*)smem;
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kv = blockIdx.x % a.kv_heads;
+  const AttnTile t = a.by_query[blockIdx.x / a.kv_heads];
+  const int end = min(t.len, t.first + kFarRows);
+  if (t.first % kFarRows != 0 || end <= a.window) return;  // no chunk's first tile, or all within their windows
+  AttnTile rows = t;
+  rows.first = max(t.first, a.window / kAttnStep * kAttnStep);
+  const int nq = (end - rows.first + kAttnStep - 1) / kAttnStep;
+  const int total = nq * (a.heads / a.kv_heads);
+  const int part = wave % a.far_parts, wk0 = wave / a.far_parts * 32;
+  const int key = wk0 + (lane & 31);
+  const float c = a.scale * kAttnLog2e;
+  const FragOff fo = frag_offsets(lane);
+  QueryStream<DP, EXACT, 4> stream(a, rows, kv, nq, wave, lane);
+  int q0 = stream.row, head = 0, cur = 0;
+  stream.template next<2>(t.len, lds, wave);
+  const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
+  const int keys = min(t.len, a.sinks) - wk0;
+  bf16x8_t kf[G::KS], vf[G::KS];
+  own_rows<DP>(a.k.p + (krow0 * a.k.ts + kv * a.k.hs) * 2, a.k.ts, a.head_dim, keys, lane, kf);
+  own_rows<DP>(a.v.p + (krow0 * a.v.ts + kv * a.v.hs) * 2, a.v.ts, a.head_dim, keys, lane, vf);
+  f32x16_t dk[G::DB], dv[G::DB];
+#pragma unroll
+  for (int db = 0; db < G::DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
+  for (int it = 0; it < total; ++it) {
+    next_tile();
+    if (it + 1 < total) stream.template next<2>(t.len, lds, wave);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int qs = q0 + 32 * b;
+      if (a.far_parts > 1 && b != (part & 1)) continue;             // another wave's half
+      if (a.far_parts > 2 && (it & 1) != (part >> 1)) continue;     // or tile
+      if (keys <= 0 || qs + 31 < a.window || qs >= t.len) continue;
+      f32x16_t s, dp;
+      dkv_scores<DP>(lds + cur, fo, b, kf, vf, s, dp);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int q = qs + res_row(r, h);
+        if (q - key < a.window || q >= t.len || key >= a.sinks) s[r] = -kInf;
+      }
+      dkv_softmax<DP>(lds + cur, b, h, c, s, dp);
+      const bf16x8_t p[2] = {to_operand(s, 0), to_operand(s, 1)}, ds[2] = {to_operand(dp, 0), to_operand(dp, 1)};
+      dkv_sums<DP>(lds + cur + G::TILEB, fo, b, p, dv);
+      dkv_sums<DP>(lds + cur, fo, b, ds, dk);
+    }
+    cur = L::STAGE - cur;
+    if (++head == stream.group) {
+      head = 0;
+      q0 -= kAttnStep;
+    }
+  }
+  if (key >= a.sinks) return;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float* p = far_sum(a, t.chunk + t.first / kFarRows, kv, part, which) + key * a.head_dim;
+#pragma unroll
+    for (int db = 0; db < G::DB; ++db)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int d = 32 * db + 8 * g + 4 * h;
+        const f32x16_t& x = which ? dv[db] : dk[db];
+        if (d < a.head_dim) gst(p + d, (f32x4_t){x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]});
+      }
+  }
+}
+
+template <int DP, bool EXACT>
+hipError_t far_rows(const AttnArgs& a, hipStream_t s) {
+  if (!a.far_parts) return hipSuccess;
+  hipLaunchKernelGGL((attention_far_kernel<DP, EXACT>), dim3(static_cast<uint32_t>(a.n_tiles) * a.kv_heads), dim3(256), 0, s,
+                     a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_window_attention(const AttnArgs& a, hipStream_t s) {
+  if (a.head_dim <= 64) return a.head_dim == 64 ? forward<64, true, true>(a, s) : forward<64, false, true>(a, s);
+  return a.head_dim == 128 ? forward<128, true, true>(a, s) : forward<128, false, true>(a, s);
+}
+
+hipError_t launch_window_attention_backward(const AttnArgs& a, hipStream_t s) {
+  if (a.head_dim <= 64) return a.head_dim == 64 ? backward<64, true, true>(a, s) : backward<64, false, true>(a, s);
+  return a.head_dim == 128 ? backward<128, true, true>(a, s) : backward<128, false, true>(a, s);
+}
+
+}  // namespace muon

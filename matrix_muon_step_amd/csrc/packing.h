@@ -16,6 +16,7 @@ struct muon_packing_s {
   const muon::AttnTile* by_key;
   uintptr_t lo, hi;  // the table's bytes
   int64_t longest;   // tokens of the longest sequence
+  int64_t chunks;    // kFarRows chunks of all sequences
 };
 
 namespace muon {

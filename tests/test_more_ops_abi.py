@@ -79,11 +79,12 @@ class packing_s(ctypes.Structure):
     """A packing's host side, of a device that is not there: what passes every check ends at that one."""
     _fields_ = [("device", ctypes.c_int), ("tokens", ctypes.c_int64), ("n_tiles", ctypes.c_int64),
                 ("by_query", ctypes.c_void_p), ("by_key", ctypes.c_void_p), ("lo", ctypes.c_size_t),
-                ("hi", ctypes.c_size_t), ("longest", ctypes.c_int64)]
+                ("hi", ctypes.c_size_t), ("longest", ctypes.c_int64), ("chunks", ctypes.c_int64)]
 
 
 def packing(tokens=100, tiles=1, longest=None):
-    return packing_s(77, tokens, tiles, BASE, BASE + 64, BASE, BASE + 4096, tokens if longest is None else longest)
+    longest = tokens if longest is None else longest
+    return packing_s(77, tokens, tiles, BASE, BASE + 64, BASE, BASE + 4096, longest, -(-longest // 1024))
 
 
 PASSED = (mm.MUON_ERR_HIP, mm.MUON_ERR_INVALID_ARG)   # no GPU, or not the packing's
@@ -222,3 +223,73 @@ def test_rotate_backward_arguments():
         assert L.muon_qk_norm_rotate_backward(*args, None, None, ctypes.byref(packing()), None, 0, None) == mm.MUON_ERR_INVALID_ARG
     assert L.muon_qk_norm_rotate(None, ctypes.byref(packing()), None) == mm.MUON_ERR_INVALID_ARG
     assert L.muon_qk_norm_rotate(ctypes.byref(rotate()), None, None) == mm.MUON_ERR_INVALID_ARG
+
+
+# -------------------------------------------------------- windowed attention
+def attention(heads=4, kv=2, dim=64):
+    return bd.muon_attention_t(heads_at(0, heads, dim), heads_at(1, kv, dim), heads_at(2, kv, dim), heads_at(3, heads, dim),
+                               BASE * 20, 128, BASE * 21, heads, heads, kv, dim, 0.125)
+
+
+def attention_grad(heads=4, kv=2, dim=64):
+    g = bd.muon_attention_grad_t()
+    for i, (f, h) in enumerate((("q", heads), ("k", kv), ("v", kv), ("o", heads), ("d_o", heads), ("dq", heads),
+                                ("dk", kv), ("dv", kv))):
+        setattr(g, f, heads_at(i, h, dim))
+    g.lse, g.lse_stride = BASE * 20, 128
+    g.heads, g.kv_heads, g.head_dim, g.scale = heads, kv, dim, 0.125
+    return g
+
+
+def call_window(a, window=10, sinks=4, p=None):
+    return mm.lib().muon_window_attention(ctypes.byref(a), window, sinks, ctypes.byref(p or packing()), None)
+
+
+def window_bytes(g, window=10, sinks=4, p=None):
+    return mm.lib().muon_window_attention_backward_workspace_bytes(ctypes.byref(g), window, sinks, ctypes.byref(p or packing()))
+
+
+def call_window_back(g, window=10, sinks=4, p=None, ws=BASE * 30, ws_bytes=1 << 30):
+    return mm.lib().muon_window_attention_backward(ctypes.byref(g), window, sinks, ctypes.byref(p or packing()),
+                                                   ctypes.c_void_p(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("make,call", [(attention, call_window), (attention_grad, call_window_back)])
+def test_window_refuses(make, call):
+    for window, sinks, status in ((0, 0, mm.MUON_ERR_INVALID_ARG), (-5, 0, mm.MUON_ERR_INVALID_ARG),
+                                  (10, -1, mm.MUON_ERR_INVALID_ARG), (10, 129, mm.MUON_ERR_UNSUPPORTED)):
+        assert call(make(), window, sinks) == status and mm.muon_last_error()
+        assert window_bytes(attention_grad(), window, sinks) == 0
+    for window, sinks in ((1, 0), (1, 128), (99, 4), (100, 0), (1 << 62, 128)):
+        assert passed(call(make(), window, sinks))
+    for field, value, status in (("heads", 0, mm.MUON_ERR_INVALID_ARG), ("head_dim", 12, mm.MUON_ERR_UNSUPPORTED),
+                                 ("scale", math.nan, mm.MUON_ERR_INVALID_ARG), ("lse", 0, mm.MUON_ERR_INVALID_ARG),
+                                 ("lse_stride", 99, mm.MUON_ERR_INVALID_ARG)):
+        a = make()
+        setattr(a, field, value)
+        assert call(a) == status
+    a = make()
+    a.k.data = 0
+    assert call(a) == mm.MUON_ERR_INVALID_ARG
+
+
+def test_window_workspace():
+    g = attention_grad()
+    base = mm.lib().muon_attention_backward_workspace_bytes(ctypes.byref(g), ctypes.byref(packing()))
+    assert window_bytes(g, 10, 0) == window_bytes(g, 100, 128) == window_bytes(g, 1 << 62, 5) == base
+    for sinks, times in ((1, 4), (4, 4), (32, 4), (33, 2), (64, 2), (65, 1), (128, 1)):
+        for tokens in (100, 1024, 1025, 5000):
+            p = packing(tokens)
+            rows = mm.lib().muon_attention_backward_workspace_bytes(ctypes.byref(g), ctypes.byref(p))
+            sums = -(-tokens // 1024) * 2 * times * 8 * sinks * 64
+            assert window_bytes(g, 10, sinks, p) == rows + (sums + 255) // 256 * 256
+    need = window_bytes(g)
+    assert need > base
+    assert call_window_back(g, ws_bytes=need - 1) == mm.MUON_ERR_WORKSPACE
+    assert call_window_back(g, ws=0) == mm.MUON_ERR_WORKSPACE
+    assert call_window_back(g, ws=BASE * 30 + 64) == mm.MUON_ERR_WORKSPACE
+    # the sums' end counts as the workspace's too
+    assert call_window_back(g, ws=g.dk.data - need + 256) == mm.MUON_ERR_ALIAS
+    assert passed(call_window_back(g, ws=g.dk.data - need))
+    assert mm.lib().muon_window_attention(None, 4, 0, ctypes.byref(packing()), None) == mm.MUON_ERR_INVALID_ARG
+    assert mm.lib().muon_window_attention(ctypes.byref(attention()), 4, 0, None, None) == mm.MUON_ERR_INVALID_ARG
