@@ -2,6 +2,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "api_common.h"
 #include "grad_internal.h"
@@ -58,27 +59,45 @@ muon_status_t check_norm(const double* norm, bool written, std::vector<Range>& r
   return MUON_OK;
 }
 
-// The next launch's tensors, from item i on (moved past them); false at the end.
-bool next_batch(const muon_gradient_t* items, int64_t n, int64_t& i, NormBatch& b) {
-  b.n = 0;
-  b.chunks[0] = 0;
-  for (; i < n && b.n < kNormBatch; ++i) {
-    const muon_gradient_t& t = items[i];
-    if (t.count == 0) continue;
-    const int64_t end = b.chunks[b.n] + chunks_of(t.count);
-    if (end > kMaxChunks) break;  // the first of a launch fits: MUON_MAX_GRADIENT
-    b.d[b.n] = {static_cast<const unsigned char*>(t.g), static_cast<unsigned char*>(t.out), t.count,
-                t.g_dtype == MUON_F32, t.out_dtype == MUON_F32};
-    b.chunks[++b.n] = static_cast<int32_t>(end);
+// A call's tensors in launches.
+class Batches {
+ public:
+  Batches(const muon_gradient_t* items, int64_t n) : items_(items), n_(n) {
+    for (int64_t i = 0; i < n; ++i) bytes_ += items[i].count * static_cast<int64_t>(width(items[i].g_dtype));
   }
-  return b.n > 0;
-}
+  // The next launch's tensors, from item i on with `before` bytes in front of
+  // it (both moved past them); false at the end.
+  bool next(int64_t& i, int64_t& before, NormBatch& b) const {
+    b.n = b.stream = 0;
+    b.large = bytes_ > kNormKeep;
+    b.chunks[0] = 0;
+    for (; i < n_ && b.n < kNormBatch; ++i) {
+      const muon_gradient_t& t = items_[i];
+      if (t.count == 0) continue;
+      const int64_t chunks = chunks_of(t.count), end = b.chunks[b.n] + chunks;
+      if (end > kMaxChunks) break;  // the first of a launch fits: MUON_MAX_GRADIENT
+      const int64_t w = static_cast<int64_t>(width(t.g_dtype));
+      // whole chunks of this tensor that lie in front of the last kNormKeep bytes
+      const int64_t stream = (bytes_ - kNormKeep - before) / (kNormChunk * w);
+      if (stream > 0) b.stream = static_cast<int32_t>(b.chunks[b.n] + std::min(stream, chunks));
+      before += t.count * w;
+      b.d[b.n] = {static_cast<const unsigned char*>(t.g), static_cast<unsigned char*>(t.out), t.count,
+                  t.g_dtype == MUON_F32, t.out_dtype == MUON_F32};
+      b.chunks[++b.n] = static_cast<int32_t>(end);
+    }
+    return b.n > 0;
+  }
+
+ private:
+  const muon_gradient_t* items_;
+  int64_t n_, bytes_ = 0;
+};
 
 // Sums of squares into the workspace; how many partials there are.
-hipError_t squares(const muon_gradient_t* items, int64_t n, double* partials, hipStream_t s, int* count) {
+hipError_t squares(const Batches& all, double* partials, hipStream_t s, int* count) {
   NormBatch b;
   *count = 0;
-  for (int64_t i = 0; next_batch(items, n, i, b);) {
+  for (int64_t i = 0, before = 0; all.next(i, before, b);) {
     b.earlier = *count;
     const hipError_t e = launch_grad_squares(b, partials, s);
     if (e != hipSuccess) return e;
@@ -105,7 +124,7 @@ muon_status_t muon_grad_norm(const muon_gradient_t* items, int64_t n, double* no
     const hipStream_t s = static_cast<hipStream_t>(stream);
     double* partials = static_cast<double*>(workspace);
     int count = 0;
-    hipError_t e = squares(items, n, partials, s, &count);
+    hipError_t e = squares(Batches(items, n), partials, s, &count);
     if (e == hipSuccess) e = launch_grad_norm(partials, count, norm, s);
     return e == hipSuccess ? MUON_OK : hip_fail(e, "gradient norm launch");
   });
@@ -126,15 +145,16 @@ muon_status_t muon_grad_clip(const muon_gradient_t* items, int64_t n, double max
     double* partials = static_cast<double*>(workspace);
     int count = -1;
     hipError_t e = hipSuccess;
-    if (!norm_given) e = squares(items, n, partials, s, &count);
+    const Batches all(items, n);
+    if (!norm_given) e = squares(all, partials, s, &count);
     if (e == hipSuccess && count == 0) e = launch_grad_norm(partials, 0, norm, s);
     // the last launch's tensors first: they were read last
-    std::vector<int64_t> starts;
+    std::vector<std::pair<int64_t, int64_t>> starts;
     NormBatch b;
-    for (int64_t i = 0, at = 0; next_batch(items, n, i, b); at = i) starts.push_back(at);
-    for (auto at = starts.rbegin(); at != starts.rend() && e == hipSuccess; ++at) {
-      int64_t i = *at;
-      next_batch(items, n, i, b);
+    std::pair<int64_t, int64_t> at = {0, 0};
+    for (auto end = at; all.next(end.first, end.second, b); at = end) starts.push_back(at);
+    for (auto it = starts.rbegin(); it != starts.rend() && e == hipSuccess; ++it) {
+      all.next(it->first, it->second, b);
       e = launch_grad_clip(b, partials, count, norm, max_norm, s);
     }
     return e == hipSuccess ? MUON_OK : hip_fail(e, "gradient clip launch");

@@ -14,6 +14,14 @@ constexpr int kNormGroups = 2048;
 // Tensors of a launch (descriptors travel as kernel arguments).
 constexpr int kNormBatch = 96;
 
+// What of a call's gradients may stay in the 256 MiB memory-side cache from
+// the sum to the clipping.  Calls of more read all else, and write, past the
+// caches.  Ten layers of 1600 (1.23 GB of float32 to 0.61 GB of bfloat16), sum
+// and clipping in us, with this many MB kept: none 174 + 325, 66 177 + 318,
+// 131 176 + 312, 197 177 + 304, 229 176 + 302; all accesses through the
+// caches 214 + 330, the sum's alone 197 + 291.
+constexpr int64_t kNormKeep = int64_t{224} << 20;
+
 struct NormDesc {
   const unsigned char* g;
   unsigned char* out;
@@ -25,6 +33,8 @@ struct NormBatch {
   NormDesc d[kNormBatch];
   int32_t chunks[kNormBatch + 1];  // exclusive prefix sums
   int32_t n;
+  int32_t stream;                  // chunks from the first that are read past the caches
+  int32_t large;                   // the call's gradients are more than kNormKeep
   int32_t earlier;                 // partial sums that earlier launches of the call left
 };
 

@@ -35,140 +35,128 @@ __device__ __forceinline__ double group_sum(double x) {
   return x;
 }
 
-// Eight values of a tensor from element i on, as float32 (zeros past n).  A
-// pointer need only be aligned to its element: the memory unit takes 16-byte
-// accesses at any address.
-template <bool F32>
-struct Eight;
-template <>
-struct Eight<true> {
-  float4 a, b;
+// A lane's run of elements, 16 bytes of the wider of the types that it reads
+// and writes, so that a wave's accesses are contiguous.  A pointer need only be
+// aligned to its element: the memory unit takes these accesses at any address.
+// STREAM: past the caches (nontemporal).
+template <int V, bool F32>
+struct Run {
+  static constexpr int WORDS = F32 ? V : V / 2;
+  typedef uint32_t words_t __attribute__((ext_vector_type(WORDS), aligned(4 * V / WORDS * F32 + 2 * !F32)));
+  uint32_t u[WORDS];
+  template <bool STREAM>
   __device__ __forceinline__ void load(const unsigned char* p) {
-    a = gld<float4>(p);
-    b = gld<float4>(p + 16);
+    if (STREAM) {
+      const words_t r = __builtin_nontemporal_load((const __attribute__((address_space(1))) words_t*)p);
+      __builtin_memcpy(u, &r, sizeof(u));
+    } else {
+      *this = gld<Run>(p);
+    }
   }
-  __device__ __forceinline__ void load_some(const unsigned char* p, int n) {
-    float v[8];
+  __device__ __forceinline__ void load_some(const unsigned char* p, int n) {  // zeros past n
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < n ? gld<float>(p + 4 * k) : 0.f;
-    a = {v[0], v[1], v[2], v[3]};
-    b = {v[4], v[5], v[6], v[7]};
+    for (int k = 0; k < WORDS; ++k) u[k] = 0;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (k >= n) break;
+      if (F32) u[k] = gld<uint32_t>(p + 4 * k);
+      else u[k / 2] |= static_cast<uint32_t>(gld<uint16_t>(p + 2 * k)) << (16 * (k & 1));
+    }
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  __device__ __forceinline__ float get(int k) const {
+    if (F32) return __uint_as_float(u[k]);
+    return k & 1 ? bf_hi(u[k / 2]) : bf_lo(u[k / 2]);
+  }
+  __device__ __forceinline__ void put(const float (&v)[V]) {
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k) u[k] = F32 ? __float_as_uint(v[k]) : pack_bf16(v[F32 ? 0 : 2 * k], v[F32 ? 0 : 2 * k + 1]);
+  }
+  template <bool STREAM>
+  __device__ __forceinline__ void store(unsigned char* p) const {
+    if (STREAM) {
+      words_t r;
+      __builtin_memcpy(&r, u, sizeof(u));
+      __builtin_nontemporal_store(r, (__attribute__((address_space(1))) words_t*)p);
+    } else {
+      gst(p, *this);
+    }
+  }
+  __device__ __forceinline__ void store_some(unsigned char* p, int n) const {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (k >= n) break;
+      if (F32) gst(p + 4 * k, u[k]);
+      else gst(p + 2 * k, static_cast<uint16_t>(u[k / 2] >> (16 * (k & 1))));
+    }
   }
 };
-template <>
-struct Eight<false> {
-  uint4 a;
-  __device__ __forceinline__ void load(const unsigned char* p) { a = gld<uint4>(p); }
-  __device__ __forceinline__ void load_some(const unsigned char* p, int n) {
-    uint32_t v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < n ? gld<uint16_t>(p + 2 * k) : 0u;
-    a = {v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = bf_lo(a.x), v[1] = bf_hi(a.x), v[2] = bf_lo(a.y), v[3] = bf_hi(a.y);
-    v[4] = bf_lo(a.z), v[5] = bf_hi(a.z), v[6] = bf_lo(a.w), v[7] = bf_hi(a.w);
-  }
-};
 
-template <bool F32>
-__device__ __forceinline__ void store_eight(unsigned char* p, const float (&v)[8]) {
-  if (F32) {
-    gst(p, make_float4(v[0], v[1], v[2], v[3]));
-    gst(p + 16, make_float4(v[4], v[5], v[6], v[7]));
-  } else {
-    gst(p, make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])));
-  }
-}
-template <bool F32>
-__device__ __forceinline__ void store_some(unsigned char* p, const float (&v)[8], int n) {
+// f(run, its first element, how many of its elements there are) for this
+// lane's runs of a chunk of n elements; whole chunks have all loads under way
+// before the first is used.
+template <int V, bool F32, bool STREAM, class F>
+__device__ __forceinline__ void for_runs(const unsigned char* g, int64_t n, F&& f) {
+  constexpr int W = F32 ? 4 : 2, ROUNDS = kNormChunk / V / kLanes;
+  if (n >= kNormChunk) {
+    Run<V, F32> x[ROUNDS];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (k >= n) break;
-    if (F32) gst(p + 4 * k, v[k]);
-    else gst(p + 2 * k, static_cast<uint16_t>(pack_bf16(v[k], 0.f)));
+    for (int r = 0; r < ROUNDS; ++r) x[r].template load<STREAM>(g + (r * kLanes + threadIdx.x) * (V * W));
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) f(x[r], (r * kLanes + static_cast<int>(threadIdx.x)) * V, V);
+    return;
+  }
+  for (int i = threadIdx.x * V; i < n; i += kLanes * V) {
+    Run<V, F32> x;
+    const int left = static_cast<int>(n) - i;
+    if (left >= V) x.template load<STREAM>(g + i * W);
+    else x.load_some(g + i * W, left);
+    f(x, i, left);
   }
 }
 
-// What a lane does in a chunk: kNormChunk / 8 / kLanes groups of eight.
-constexpr int kRounds = kNormChunk / 8 / kLanes;
-
-__device__ __forceinline__ void add_squares(const float (&v)[8], double (&acc)[4]) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const double d = v[k];
-    acc[k & 3] = fma(d, d, acc[k & 3]);
-  }
-}
-
-template <bool F32>
+template <bool F32, bool STREAM>
 __device__ __forceinline__ void chunk_squares(const unsigned char* g, int64_t n, double (&acc)[4]) {
-  constexpr int W = F32 ? 4 : 2;
-  float v[8];
-  if (n >= kNormChunk) {
-    Eight<F32> x[kRounds];
+  constexpr int V = F32 ? 4 : 8;
+  for_runs<V, F32, STREAM>(g, n, [&](const Run<V, F32>& x, int, int) {
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) x[r].load(g + static_cast<int64_t>(r * kLanes + threadIdx.x) * 8 * W);
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      x[r].get(v);
-      add_squares(v, acc);
+    for (int k = 0; k < V; ++k) {
+      const double d = x.get(k);
+      acc[k & 3] = fma(d, d, acc[k & 3]);
     }
-    return;
-  }
-  for (int i = threadIdx.x * 8; i < n; i += kLanes * 8) {
-    Eight<F32> x;
-    if (i + 8 <= n) x.load(g + static_cast<int64_t>(i) * W);
-    else x.load_some(g + static_cast<int64_t>(i) * W, static_cast<int>(n - i));
-    x.get(v);
-    add_squares(v, acc);
-  }
+  });
 }
 
-template <bool F32, bool OUT>
+template <bool F32, bool OUT, bool STREAM>
 __device__ __forceinline__ void chunk_scale(const unsigned char* g, unsigned char* out, int64_t n, double f) {
-  constexpr int W = F32 ? 4 : 2, O = OUT ? 4 : 2;
-  float v[8];
-  if (n >= kNormChunk) {
-    Eight<F32> x[kRounds];
+  constexpr int V = F32 || OUT ? 4 : 8, O = OUT ? 4 : 2;
+  for_runs<V, F32, STREAM>(g, n, [&](const Run<V, F32>& x, int first, int count) {
+    float v[V];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) x[r].load(g + static_cast<int64_t>(r * kLanes + threadIdx.x) * 8 * W);
-#pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      x[r].get(v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = static_cast<float>(static_cast<double>(v[k]) * f);
-      store_eight<OUT>(out + static_cast<int64_t>(r * kLanes + threadIdx.x) * 8 * O, v);
-    }
-    return;
-  }
-  for (int i = threadIdx.x * 8; i < n; i += kLanes * 8) {
-    Eight<F32> x;
-    const int left = static_cast<int>(n - i);
-    if (left >= 8) x.load(g + static_cast<int64_t>(i) * W);
-    else x.load_some(g + static_cast<int64_t>(i) * W, left);
-    x.get(v);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = static_cast<float>(static_cast<double>(v[k]) * f);
-    if (left >= 8) store_eight<OUT>(out + static_cast<int64_t>(i) * O, v);
-    else store_some<OUT>(out + static_cast<int64_t>(i) * O, v, left);
-  }
+    for (int k = 0; k < V; ++k) v[k] = static_cast<float>(static_cast<double>(x.get(k)) * f);
+    Run<V, OUT> y;
+    y.put(v);
+    if (count >= V) y.template store<STREAM>(out + first * O);
+    else y.store_some(out + first * O, count);
+  });
 }
 
-// Work-group w takes chunks w, w + gridDim.x, ... of the batch.
+// Work-group w takes chunks w, w + gridDim.x, ... of the batch.  The first
+// b.stream of them go past the caches, so that the memory-side cache is left
+// to the last ones, which clipping reads first.
 __global__ __launch_bounds__(kLanes) void grad_squares_kernel(const NormBatch b, double* partials) {
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
   const int total = b.chunks[b.n];
   for (int c = blockIdx.x; c < total; c += gridDim.x) {
     const int i = find_mat(b.chunks, b.n, c);
     const NormDesc& d = b.d[i];
-    const int64_t first = static_cast<int64_t>(c - b.chunks[i]) * kNormChunk;
-    if (d.g_f32) chunk_squares<true>(d.g + first * 4, d.count - first, acc);
-    else chunk_squares<false>(d.g + first * 2, d.count - first, acc);
+    const int64_t first = static_cast<int64_t>(c - b.chunks[i]) * kNormChunk, left = d.count - first;
+    if (d.g_f32) {
+      if (c < b.stream) chunk_squares<true, true>(d.g + first * 4, left, acc);
+      else chunk_squares<true, false>(d.g + first * 4, left, acc);
+    } else {
+      if (c < b.stream) chunk_squares<false, true>(d.g + first * 2, left, acc);
+      else chunk_squares<false, false>(d.g + first * 2, left, acc);
+    }
   }
   const double sum = group_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
   if (threadIdx.x == 0) {
@@ -190,7 +178,8 @@ __global__ __launch_bounds__(kLanes) void grad_norm_kernel(const double* partial
 }
 
 // From the last chunk to the first, since the last ones that the sum read are
-// the likeliest to be in the memory-side cache still.
+// in the memory-side cache still.  STREAM: reads and writes go past the caches.
+template <bool STREAM>
 __global__ __launch_bounds__(kLanes) void grad_clip_kernel(const NormBatch b, const double* partials, int n, double* norm,
                                                            double max_norm) {
   double x;
@@ -209,11 +198,11 @@ __global__ __launch_bounds__(kLanes) void grad_clip_kernel(const NormBatch b, co
     if (!clip && d.out == d.g) continue;  // in place, and as it is
     const int64_t first = static_cast<int64_t>(c - b.chunks[i]) * kNormChunk, left = d.count - first;
     if (d.g_f32) {
-      if (d.out_f32) chunk_scale<true, true>(d.g + first * 4, d.out + first * 4, left, f);
-      else chunk_scale<true, false>(d.g + first * 4, d.out + first * 2, left, f);
+      if (d.out_f32) chunk_scale<true, true, STREAM>(d.g + first * 4, d.out + first * 4, left, f);
+      else chunk_scale<true, false, STREAM>(d.g + first * 4, d.out + first * 2, left, f);
     } else {
-      if (d.out_f32) chunk_scale<false, true>(d.g + first * 2, d.out + first * 4, left, f);
-      else chunk_scale<false, false>(d.g + first * 2, d.out + first * 2, left, f);
+      if (d.out_f32) chunk_scale<false, true, STREAM>(d.g + first * 2, d.out + first * 4, left, f);
+      else chunk_scale<false, false, STREAM>(d.g + first * 2, d.out + first * 2, left, f);
     }
   }
 }
@@ -237,7 +226,8 @@ hipError_t launch_grad_norm(const double* partials, int n, double* norm, hipStre
 
 hipError_t launch_grad_clip(const NormBatch& b, const double* partials, int n, double* norm, double max_norm,
                             hipStream_t s) {
-  hipLaunchKernelGGL(grad_clip_kernel, groups(b), dim3(kLanes), 0, s, b, partials, n, norm, max_norm);
+  const auto kernel = b.large ? grad_clip_kernel<true> : grad_clip_kernel<false>;
+  hipLaunchKernelGGL(kernel, groups(b), dim3(kLanes), 0, s, b, partials, n, norm, max_norm);
   return hipGetLastError();
 }
 

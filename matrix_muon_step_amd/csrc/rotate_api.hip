@@ -112,12 +112,15 @@ muon_status_t check(const Call& c, muon_packing_t packing, const std::vector<Ran
   return check_aliasing(others);
 }
 
+bool is_wide(const muon_qk_rotate_t& a) {
+  return a.rotary.rotary_dim % 16 == 0 && (a.head_dim - a.rotary.rotary_dim) % 16 == 0;
+}
+
 RotateArgs arguments(const Call& c, muon_packing_t packing) {
   const muon_qk_rotate_t& a = *c.a;
   RotateArgs r;
   memset(&r, 0, sizeof(r));
-  const bool wide = a.rotary.rotary_dim % 16 == 0 && (a.head_dim - a.rotary.rotary_dim) % 16 == 0;
-  const int lanes = a.head_dim / (wide ? 16 : 8);
+  const int lanes = a.head_dim / (is_wide(a) ? 16 : 8);
   while ((1 << r.group_log2) < lanes) ++r.group_log2;
   const int slots = kRotateLanes >> r.group_log2;
   for (int i = 0; i < 2; ++i) {
@@ -146,8 +149,17 @@ RotateArgs arguments(const Call& c, muon_packing_t packing) {
   return r;
 }
 
-bool is_wide(const muon_qk_rotate_t& a) {
-  return a.rotary.rotary_dim % 16 == 0 && (a.head_dim - a.rotary.rotary_dim) % 16 == 0;
+// Whether the tensors of a call are more than the memory-side cache holds.
+bool is_large(const Call& c, int64_t tokens) {
+  const int64_t tensors = c.backward && c.a->norm ? 3 : 2;
+  return tensors * tokens * (c.a->heads + c.a->kv_heads) * c.a->head_dim * 2 > kRotateLarge;
+}
+
+hipError_t launch(const Call& c, muon_packing_t packing, float* partials, void* stream) {
+  RotateArgs r = arguments(c, packing);
+  r.partials = partials;
+  return launch_rotate(r, {c.backward, is_wide(*c.a), c.a->rotary.interleaved != 0, c.a->norm != 0, is_large(c, packing->tokens)},
+                       static_cast<hipStream_t>(stream));
 }
 
 size_t partial_bytes(int32_t head_dim) { return align_up(static_cast<size_t>(kRotateGroups) * 2 * head_dim * sizeof(float)); }
@@ -163,8 +175,7 @@ muon_status_t muon_qk_norm_rotate(const muon_qk_rotate_t* args, muon_packing_t p
     muon_status_t st = check(c, packing, {});
     if (st == MUON_OK) st = check_device(packing);
     if (st != MUON_OK || packing->n_tiles == 0) return st;
-    const hipError_t e = launch_rotate(arguments(c, packing), is_wide(*args), args->rotary.interleaved != 0, args->norm != 0,
-                                       static_cast<hipStream_t>(stream));
+    const hipError_t e = launch(c, packing, nullptr, stream);
     return e == hipSuccess ? MUON_OK : hip_fail(e, "norm and rotation launch");
   });
 }
@@ -200,10 +211,7 @@ muon_status_t muon_qk_norm_rotate_backward(const muon_qk_rotate_t* args, const m
     muon_status_t st = check(c, packing, more);
     if (st == MUON_OK) st = check_device(packing);
     if (st != MUON_OK || (packing->n_tiles == 0 && !sums)) return st;
-    RotateArgs r = arguments(c, packing);
-    r.partials = static_cast<float*>(workspace);
-    const hipError_t e = launch_rotate_backward(r, is_wide(*args), args->rotary.interleaved != 0, args->norm != 0,
-                                                static_cast<hipStream_t>(stream));
+    const hipError_t e = launch(c, packing, static_cast<float*>(workspace), stream);
     return e == hipSuccess ? MUON_OK : hip_fail(e, "norm and rotation backward launch");
   });
 }

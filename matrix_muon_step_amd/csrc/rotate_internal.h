@@ -13,6 +13,7 @@ constexpr int kRotatePieces = kAttnRows / kRotateRows;
 // with one partial sum of the weights' gradients in the workspace.
 constexpr int kRotateGroups = 1024;
 constexpr int kRotateLanes = 256;
+constexpr int64_t kRotateLarge = int64_t{256} << 20;
 
 // One of the two tensors of a call.
 struct RotateTensor {
@@ -39,8 +40,15 @@ struct RotateArgs {
   uint8_t axis[kAttnMaxDim / 2];
 };
 
-// wide: eight pairs to a lane (rotary_dim and head_dim - rotary_dim multiples of 16), else four.
-hipError_t launch_rotate(const RotateArgs& a, bool wide, bool interleaved, bool norm, hipStream_t s);
-hipError_t launch_rotate_backward(const RotateArgs& a, bool wide, bool interleaved, bool norm, hipStream_t s);
+// Which kernel serves a call.
+struct RotateForm {
+  bool back;         // the gradient
+  bool wide;         // eight pairs to a lane (rotary_dim and head_dim - rotary_dim multiples of 16), else four
+  bool interleaved;
+  bool norm;
+  bool large;        // more bytes than the caches hold: reads and writes past them
+};
+// Launches it and, where a weight's gradient is asked for, the kernel that joins its sums.
+hipError_t launch_rotate(const RotateArgs& a, const RotateForm& f, hipStream_t s);
 
 }  // namespace muon

@@ -110,6 +110,7 @@ struct Place {
   __device__ __forceinline__ Place(const RotateArgs& a, int c) {
     const int R = a.rotary_dim, D = a.head_dim;
     live = c * 2 * P < D;
+    if (!live) c = 0;
     turned = c * 2 * P < R;
     pair = c * P;
     if (INTER) {
@@ -149,38 +150,53 @@ struct Place {
   }
 };
 
-// A lane's way through the (token, head) pairs of a piece.
+// A lane's way through the (token, head) pairs of a piece, with its place in
+// each of N tensors.  Past its last head it stays there, where loads are
+// harmless; so do the loads of lanes that hold no part of a head (as lane 0's).
+template <int N>
 struct Walk {
-  int token, head, left;  // left: heads from here to the piece's end
-  __device__ __forceinline__ Walk(int slot, int heads, int n) {
+  unsigned char* p[N];
+  int64_t step[N], wrap[N];  // bytes to the next head; from behind a token's last head to the next token
+  int token, head, left;     // left: heads from here to the piece's end
+  int heads, step_token, step_head, slots;
+  __device__ __forceinline__ Walk(const RotateTensor& t, const HeadsView (&v)[N], int64_t row, int slot, int slots_, int n) {
+    heads = t.heads, step_token = t.step_token, step_head = t.step_head, slots = slots_;
+    left = n * heads - slot;
+    if (left <= 0) slot = 0;
     token = slot / heads;
     head = slot - token * heads;
-    left = n * heads - slot;
-  }
-  __device__ __forceinline__ void next(const RotateTensor& t, int slots) {
-    token += t.step_token;
-    head += t.step_head;
-    if (head >= t.heads) {
-      head -= t.heads;
-      ++token;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      p[i] = v[i].p + ((row + token) * v[i].ts + head * v[i].hs) * 2;
+      step[i] = (step_token * v[i].ts + step_head * v[i].hs) * 2;
+      wrap[i] = (v[i].ts - heads * v[i].hs) * 2;
     }
+  }
+  __device__ __forceinline__ void next() {
     left -= slots;
+    if (left <= 0) return;
+    token += step_token;
+    head += step_head;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] += step[i];
+    if (head >= heads) {
+      head -= heads;
+      ++token;
+#pragma unroll
+      for (int i = 0; i < N; ++i) p[i] += wrap[i];
+    }
   }
 };
-
-__device__ __forceinline__ unsigned char* at(const HeadsView& v, int64_t row, int token, int head) {
-  return v.p + ((row + token) * v.ts + head * v.hs) * 2;
-}
 
 // 1 / sqrt(mean x^2 + eps) of the head that x is a lane's part of.  Where the
 // squares of finite values overflow, x is scaled by 2^-72 and the result
 // belongs to the scaled x (eps is nothing beside it); `back` is that scale, or 1.
 template <int N>
-__device__ __forceinline__ float inverse_size(const RotateArgs& a, float (&x)[N], float& back) {
+__device__ __forceinline__ float inverse_size(const RotateArgs& a, bool live, float (&x)[N], float& back) {
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) sum = fmaf(x[i], x[i], sum);
-  sum = head_sum(sum, a.group_log2);
+  sum = head_sum(live ? sum : 0.f, a.group_log2);
   back = 1.f;
   const float share = 1.f / static_cast<float>(a.head_dim);
   if (__builtin_expect(sum == kInf, 0)) {
@@ -191,203 +207,213 @@ __device__ __forceinline__ float inverse_size(const RotateArgs& a, float (&x)[N]
       x[i] *= back;
       sum = fmaf(x[i], x[i], sum);
     }
-    sum = head_sum(sum, a.group_log2);
+    sum = head_sum(live ? sum : 0.f, a.group_log2);
     return __builtin_amdgcn_rsqf(sum * share);
   }
   return __builtin_amdgcn_rsqf(fmaf(sum, share, a.eps));
 }
 
 template <int P>
-__device__ __forceinline__ void load_weight(const float* w, int lo, int hi, bool live, float (&v)[2 * P]) {
+__device__ __forceinline__ void load_weight(const float* w, int lo, int hi, float (&v)[2 * P]) {
 #pragma unroll
-  for (int i = 0; i < 2 * P; ++i) v[i] = w && live ? gld<float>(w + (i < P ? lo + i : hi + i - P)) : 1.f;
+  for (int i = 0; i < 2 * P; ++i) v[i] = w ? gld<float>(w + (i < P ? lo + i : hi + i - P)) : 1.f;
 }
 
+// A work item's rows, and none for pieces past a sequence's end.
+struct Piece {
+  int64_t row;   // packed row of its first token
+  int index, n;  // that token's index in its sequence; tokens
+  __device__ __forceinline__ Piece(const RotateArgs& a, int64_t i) {
+    const AttnTile t = a.tiles[i / kRotatePieces];
+    index = t.first + static_cast<int>(i % kRotatePieces) * kRotateRows;
+    n = min(t.len - index, kRotateRows);
+    row = static_cast<int64_t>(t.row0) + index;
+  }
+};
+
+// A lane's part of one head of one token.  STREAM: past the caches (see is_large).
+template <int P>
+struct Part {
+  typedef uint32_t words_t __attribute__((ext_vector_type(P / 2)));
+  Raw<P> lo, hi;
+  __device__ __forceinline__ void load(const unsigned char* p, int at_lo, int at_hi) {
+    lo = gld<Raw<P>>(p + at_lo);
+    hi = gld<Raw<P>>(p + at_hi);
+  }
+  template <bool STREAM>
+  __device__ __forceinline__ void store(unsigned char* p, int at_lo, int at_hi) const {
+    if (STREAM) {
+      words_t l, h;
+      __builtin_memcpy(&l, &lo, sizeof(lo));
+      __builtin_memcpy(&h, &hi, sizeof(hi));
+      __builtin_nontemporal_store(l, (__attribute__((address_space(1))) words_t*)(p + at_lo));
+      __builtin_nontemporal_store(h, (__attribute__((address_space(1))) words_t*)(p + at_hi));
+    } else {
+      gst(p + at_lo, lo);
+      gst(p + at_hi, hi);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[2 * P]) const {
+    lo.get(v);
+    hi.get(v + P);
+  }
+  __device__ __forceinline__ void put(const float (&v)[2 * P]) {
+    lo.put(v);
+    hi.put(v + P);
+  }
+};
+
 // ------------------------------------------------------------------ forward
-template <int P, bool INTER, bool NORM>
+// Queries and keys in work-groups of their own (blockIdx.y), here and in the
+// backward pass: twice as many for short calls, one weight (and its gradient)
+// in registers at a time.
+template <int P, bool INTER, bool NORM, bool STREAM>
 __global__ __launch_bounds__(kRotateLanes) void rotate_kernel(const RotateArgs a) {
-  constexpr int U = 2;  // heads a lane has under way
   __shared__ __align__(16) Angles angles;
+  const RotateTensor& t = a.t[blockIdx.y];
   const int slots = kRotateLanes >> a.group_log2, slot = threadIdx.x >> a.group_log2;
   const Place<P, INTER> place(a, threadIdx.x & ((1 << a.group_log2) - 1));
-  const int half = a.rotary_dim >> 1;
-  for (int64_t piece = blockIdx.x; piece < int64_t{a.n_tiles} * kRotatePieces; piece += gridDim.x) {
-    const AttnTile t = a.tiles[piece / kRotatePieces];
-    const int index = t.first + static_cast<int>(piece % kRotatePieces) * kRotateRows;
-    const int n = min(t.len - index, kRotateRows);
-    if (n <= 0) continue;
-    const int64_t row = static_cast<int64_t>(t.row0) + index;
+  const int half = a.rotary_dim >> 1, lo = 2 * place.lo, hi = 2 * place.hi;
+  const int64_t pieces = int64_t{a.n_tiles} * kRotatePieces;
+  float w[2 * P];
+  if (NORM) load_weight<P>(t.weight, place.lo, place.hi, w);
+  for (int64_t i = blockIdx.x; i < pieces; i += gridDim.x) {
+    const Piece piece(a, i);
+    if (piece.n <= 0) continue;
+    Walk<2> walk(t, {t.x, t.out}, piece.row, slot, slots, piece.n);
+    Part<P> now, next;
+    now.load(walk.p[0], lo, hi);
     __syncthreads();  // the last piece's angles are done with
-    fill_angles(a, row, index, n, angles);
+    fill_angles(a, piece.row, piece.index, piece.n, angles);
     __syncthreads();
+    while (walk.left > 0) {
+      unsigned char* out = walk.p[1];
+      const int token = walk.token;
+      walk.next();
+      next.load(walk.p[0], lo, hi);
+      float v[2 * P];
+      now.get(v);
+      if (NORM) {
+        float back;
+        const float r = inverse_size<2 * P>(a, place.live, v, back);
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const RotateTensor& x = a.t[which];
-      float w[2 * P];
-      if (NORM) load_weight<P>(x.weight, place.lo, place.hi, place.live, w);
-      Walk walk(slot, x.heads, n);
-      while (walk.left > 0) {
-        Raw<P> lo[U], hi[U];
-        int token[U], head[U];
-        bool on[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          token[u] = walk.token, head[u] = walk.head;
-          on[u] = walk.left > 0 && place.live;
-          if (on[u]) {
-            const unsigned char* p = at(x.x, row, token[u], head[u]);
-            lo[u] = gld<Raw<P>>(p + place.lo * 2);
-            hi[u] = gld<Raw<P>>(p + place.hi * 2);
-          } else {
-            lo[u] = hi[u] = Raw<P>{};
-          }
-          walk.next(x, slots);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float v[2 * P];
-          lo[u].get(v);
-          hi[u].get(v + P);
-          if (NORM) {
-            float back;
-            const float r = inverse_size<2 * P>(a, v, back);
-#pragma unroll
-            for (int i = 0; i < 2 * P; ++i) v[i] = v[i] * r * w[i];
-          }
-          if (!on[u]) continue;
-          place.template turn<false>(angles, token[u] * half, v);
-          lo[u].put(v);
-          hi[u].put(v + P);
-          unsigned char* p = at(x.out, row, token[u], head[u]);
-          gst(p + place.lo * 2, lo[u]);
-          gst(p + place.hi * 2, hi[u]);
-        }
+        for (int k = 0; k < 2 * P; ++k) v[k] = v[k] * r * w[k];
       }
+      place.template turn<false>(angles, token * half, v);
+      now.put(v);
+      if (place.live) now.template store<STREAM>(out, lo, hi);
+      now = next;
     }
   }
 }
 
 // ----------------------------------------------------------------- backward
 // Without a norm the gradient is dz turned back.
-template <int P, bool INTER, bool NORM>
-__global__ __launch_bounds__(kRotateLanes) void rotate_backward_kernel(const RotateArgs a) {
-  constexpr int U = 2;
+template <int P, bool INTER, bool NORM, bool STREAM>
+__global__ __launch_bounds__(kRotateLanes, 4) void rotate_backward_kernel(const RotateArgs a) {
   __shared__ __align__(16) Angles angles;
+  const RotateTensor& t = a.t[blockIdx.y];
   const int slots = kRotateLanes >> a.group_log2, slot = threadIdx.x >> a.group_log2;
   const Place<P, INTER> place(a, threadIdx.x & ((1 << a.group_log2) - 1));
-  const int half = a.rotary_dim >> 1;
-  const float share = 1.f / static_cast<float>(a.head_dim);
-  float dw[2][2 * P];
+  const int half = a.rotary_dim >> 1, lo = 2 * place.lo, hi = 2 * place.hi, D = a.head_dim;
+  const float share = 1.f / static_cast<float>(D);
+  const int64_t pieces = int64_t{a.n_tiles} * kRotatePieces;
+  float w[2 * P], dw[2 * P];
+  if (NORM) load_weight<P>(t.weight, place.lo, place.hi, w);
 #pragma unroll
-  for (int i = 0; i < 2 * P; ++i) dw[0][i] = dw[1][i] = 0.f;
-  for (int64_t piece = blockIdx.x; piece < int64_t{a.n_tiles} * kRotatePieces; piece += gridDim.x) {
-    const AttnTile t = a.tiles[piece / kRotatePieces];
-    const int index = t.first + static_cast<int>(piece % kRotatePieces) * kRotateRows;
-    const int n = min(t.len - index, kRotateRows);
-    if (n <= 0) continue;
-    const int64_t row = static_cast<int64_t>(t.row0) + index;
+  for (int k = 0; k < 2 * P; ++k) dw[k] = 0.f;
+  for (int64_t i = blockIdx.x; i < pieces; i += gridDim.x) {
+    const Piece piece(a, i);
+    if (piece.n <= 0) continue;
+    Walk<3> walk(t, {t.up, t.out, NORM ? t.x : t.up}, piece.row, slot, slots, piece.n);
+    Part<P> up, up_next, x, x_next;
+    up.load(walk.p[0], lo, hi);
+    if (NORM) x.load(walk.p[2], lo, hi);
     __syncthreads();
-    fill_angles(a, row, index, n, angles);
+    fill_angles(a, piece.row, piece.index, piece.n, angles);
     __syncthreads();
+    while (walk.left > 0) {
+      unsigned char* out = walk.p[1];
+      const int token = walk.token;
+      walk.next();
+      up_next.load(walk.p[0], lo, hi);
+      if (NORM) x_next.load(walk.p[2], lo, hi);
+      float g[2 * P];
+      up.get(g);
+      place.template turn<true>(angles, token * half, g);
+      if (NORM) {
+        float v[2 * P], back;
+        x.get(v);
+        const float r = inverse_size<2 * P>(a, place.live, v, back);
+        float along = 0.f;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const RotateTensor& x = a.t[which];
-      float w[2 * P];
-      if (NORM) load_weight<P>(x.weight, place.lo, place.hi, place.live, w);
-      Walk walk(slot, x.heads, n);
-      while (walk.left > 0) {
-        Raw<P> lo[U], hi[U], glo[U], ghi[U];
-        int token[U], head[U];
-        bool on[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          token[u] = walk.token, head[u] = walk.head;
-          on[u] = walk.left > 0 && place.live;
-          lo[u] = hi[u] = glo[u] = ghi[u] = Raw<P>{};
-          if (on[u]) {
-            const unsigned char* p = at(x.up, row, token[u], head[u]);
-            glo[u] = gld<Raw<P>>(p + place.lo * 2);
-            ghi[u] = gld<Raw<P>>(p + place.hi * 2);
-            if (NORM) {
-              const unsigned char* px = at(x.x, row, token[u], head[u]);
-              lo[u] = gld<Raw<P>>(px + place.lo * 2);
-              hi[u] = gld<Raw<P>>(px + place.hi * 2);
-            }
-          }
-          walk.next(x, slots);
+        for (int k = 0; k < 2 * P; ++k) {
+          v[k] *= r;
+          dw[k] = fmaf(g[k], v[k], dw[k]);
+          g[k] *= w[k];
+          along = fmaf(g[k], v[k], along);
         }
+        along = head_sum(place.live ? along : 0.f, a.group_log2) * share;
+        const float scale = r * back;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float g[2 * P];
-          glo[u].get(g);
-          ghi[u].get(g + P);
-          // lanes that hold nothing (zeros) go along up to the sums over lanes
-          if (on[u]) place.template turn<true>(angles, token[u] * half, g);
-          if (NORM) {
-            float v[2 * P], back;
-            lo[u].get(v);
-            hi[u].get(v + P);
-            const float r = inverse_size<2 * P>(a, v, back);
-            float along = 0.f;
-#pragma unroll
-            for (int i = 0; i < 2 * P; ++i) {
-              v[i] *= r;
-              if (on[u]) dw[which][i] = fmaf(g[i], v[i], dw[which][i]);
-              g[i] *= w[i];
-              along = fmaf(g[i], v[i], along);
-            }
-            along = head_sum(along, a.group_log2) * share;
-#pragma unroll
-            for (int i = 0; i < 2 * P; ++i) g[i] = r * back * fmaf(-along, v[i], g[i]);
-          }
-          if (!on[u]) continue;
-          glo[u].put(g);
-          ghi[u].put(g + P);
-          unsigned char* p = at(x.out, row, token[u], head[u]);
-          gst(p + place.lo * 2, glo[u]);
-          gst(p + place.hi * 2, ghi[u]);
-        }
+        for (int k = 0; k < 2 * P; ++k) g[k] = scale * fmaf(-along, v[k], g[k]);
+        x = x_next;
       }
+      up.put(g);
+      if (place.live) up.template store<STREAM>(out, lo, hi);
+      up = up_next;
     }
   }
-  if (!NORM || (!a.t[0].d_weight && !a.t[1].d_weight)) return;
-  // This work-group's sums over its lanes, in a fixed order.
-  __shared__ float part[kRotateLanes / 64][2][kAttnMaxDim];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (!NORM || !t.d_weight) return;
+  // This work-group's sums over its lanes, in a fixed order: an element's from
+  // every slot, by as many lanes as there are for it.
+  __shared__ float part[kRotateLanes * 2 * P], sums[kRotateLanes];
+  if (place.live) {
 #pragma unroll
-  for (int which = 0; which < 2; ++which)
-#pragma unroll
-    for (int i = 0; i < 2 * P; ++i) {
-      float x = dw[which][i];
-      for (int off = 32; off >= 1 << a.group_log2; off >>= 1) x += __shfl_xor(x, off, 64);
-      if (lane < 1 << a.group_log2 && place.live) part[wave][which][i < P ? place.lo + i : place.hi + i - P] = x;
-    }
+    for (int k = 0; k < 2 * P; ++k) part[slot * D + (k < P ? place.lo + k : place.hi + k - P)] = dw[k];
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * a.head_dim; i += kRotateLanes) {
-    const int which = i >= a.head_dim, d = i - which * a.head_dim;
+  const int shares = kRotateLanes / D, mine = threadIdx.x / D, d = threadIdx.x - mine * D;
+  if (mine < shares) {
     float x = 0.f;
-#pragma unroll
-    for (int v = 0; v < kRotateLanes / 64; ++v) x += part[v][which][d];
-    gst(a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.head_dim + i, x);
+#pragma unroll 8
+    for (int v = mine; v < slots; v += shares) x += part[v * D + d];
+    sums[threadIdx.x] = x;
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float x = sums[d];
+    for (int v = 1; v < shares; ++v) x += sums[v * D + d];
+    gst(a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + blockIdx.y) * D + d, x);
   }
 }
 
 // The weights' gradients from the work-groups' sums, in float64: 16 elements
-// of one tensor to a work-group, 16 lanes to an element.
-__global__ __launch_bounds__(256) void rotate_weights_kernel(const RotateArgs a, int groups) {
-  __shared__ double part[16][16];
+// of one tensor to a work-group, 64 lanes to four of them.
+constexpr int kJoinLanes = 256, kJoinElements = 16;
+__global__ __launch_bounds__(kJoinLanes) void rotate_weights_kernel(const RotateArgs a, int groups) {
+  constexpr int R = kJoinLanes / (kJoinElements / 4);
+  __shared__ double part[R][kJoinElements + 1];
   float* out = a.t[blockIdx.y].d_weight;
-  const int e = threadIdx.x & 15, r = threadIdx.x >> 4, d = blockIdx.x * 16 + e;
-  double x = 0.0;
-  if (d < a.head_dim && out)
-    for (int i = r; i < groups; i += 16)
-      x += gld<float>(a.partials + (static_cast<int64_t>(i) * 2 + blockIdx.y) * a.head_dim + d);
-  part[r][e] = x;
-  __syncthreads();
-  if (r > 0 || d >= a.head_dim || !out) return;
+  const int e = threadIdx.x % (kJoinElements / 4) * 4, r = threadIdx.x / (kJoinElements / 4), d = blockIdx.x * kJoinElements + e;
+  double x[4] = {0.0, 0.0, 0.0, 0.0};
+  if (d < a.head_dim && out) {
+    const float* p = a.partials + blockIdx.y * a.head_dim + d;
+#pragma unroll 8
+    for (int i = r; i < groups; i += R) {
+      const float4 v = gld<float4>(p + static_cast<int64_t>(i) * 2 * a.head_dim);
+      x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+    }
+  }
 #pragma unroll
-  for (int i = 1; i < 16; ++i) x += part[i][e];
-  gst(out + d, static_cast<float>(x));
+  for (int k = 0; k < 4; ++k) part[r][e + k] = x[k];
+  __syncthreads();
+  const int o = blockIdx.x * kJoinElements + threadIdx.x;
+  if (threadIdx.x >= kJoinElements || o >= a.head_dim || !out) return;
+  double sum = 0.0;
+#pragma unroll 8
+  for (int i = 0; i < R; ++i) sum += part[i][threadIdx.x];
+  gst(out + o, static_cast<float>(sum));
 }
 
 uint32_t groups_of(const RotateArgs& a, int64_t most) {
@@ -395,44 +421,32 @@ uint32_t groups_of(const RotateArgs& a, int64_t most) {
   return static_cast<uint32_t>(pieces < most ? pieces : most);
 }
 
-template <int P, bool INTER, bool NORM>
-void forward(const RotateArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((rotate_kernel<P, INTER, NORM>), dim3(groups_of(a, 1 << 20)), dim3(kRotateLanes), 0, s, a);
+template <int P, bool INTER, bool NORM, bool STREAM>
+void launch(const RotateArgs& a, bool back, hipStream_t s) {
+  if (back)
+    hipLaunchKernelGGL((rotate_backward_kernel<P, INTER, NORM, STREAM>), dim3(groups_of(a, kRotateGroups), 2),
+                       dim3(kRotateLanes), 0, s, a);
+  else
+    hipLaunchKernelGGL((rotate_kernel<P, INTER, NORM, STREAM>), dim3(groups_of(a, 1 << 20), 2), dim3(kRotateLanes), 0, s, a);
 }
-template <int P, bool INTER, bool NORM>
-void backward(const RotateArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((rotate_backward_kernel<P, INTER, NORM>), dim3(groups_of(a, kRotateGroups)), dim3(kRotateLanes), 0, s,
-                     a);
+template <int P, bool INTER>
+void launch(const RotateArgs& a, bool norm, bool large, bool back, hipStream_t s) {
+  if (norm) large ? launch<P, INTER, true, true>(a, back, s) : launch<P, INTER, true, false>(a, back, s);
+  else large ? launch<P, INTER, false, true>(a, back, s) : launch<P, INTER, false, false>(a, back, s);
 }
 
 }  // namespace
 
-hipError_t launch_rotate(const RotateArgs& a, bool wide, bool interleaved, bool norm, hipStream_t s) {
-  if (wide) {
-    if (interleaved) norm ? forward<8, true, true>(a, s) : forward<8, true, false>(a, s);
-    else norm ? forward<8, false, true>(a, s) : forward<8, false, false>(a, s);
-  } else {
-    if (interleaved) norm ? forward<4, true, true>(a, s) : forward<4, true, false>(a, s);
-    else norm ? forward<4, false, true>(a, s) : forward<4, false, false>(a, s);
-  }
-  return hipGetLastError();
-}
-
-hipError_t launch_rotate_backward(const RotateArgs& a, bool wide, bool interleaved, bool norm, hipStream_t s) {
-  hipError_t e = hipSuccess;
+hipError_t launch_rotate(const RotateArgs& a, const RotateForm& f, hipStream_t s) {
   if (a.n_tiles > 0) {
-    if (wide) {
-      if (interleaved) norm ? backward<8, true, true>(a, s) : backward<8, true, false>(a, s);
-      else norm ? backward<8, false, true>(a, s) : backward<8, false, false>(a, s);
-    } else {
-      if (interleaved) norm ? backward<4, true, true>(a, s) : backward<4, true, false>(a, s);
-      else norm ? backward<4, false, true>(a, s) : backward<4, false, false>(a, s);
-    }
-    e = hipGetLastError();
+    if (f.wide) f.interleaved ? launch<8, true>(a, f.norm, f.large, f.back, s) : launch<8, false>(a, f.norm, f.large, f.back, s);
+    else f.interleaved ? launch<4, true>(a, f.norm, f.large, f.back, s) : launch<4, false>(a, f.norm, f.large, f.back, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  if (e != hipSuccess || (!a.t[0].d_weight && !a.t[1].d_weight)) return e;
-  hipLaunchKernelGGL(rotate_weights_kernel, dim3((a.head_dim + 15) / 16, 2), dim3(256), 0, s, a,
-                     static_cast<int>(groups_of(a, kRotateGroups)));
+  if (!a.t[0].d_weight && !a.t[1].d_weight) return hipSuccess;
+  hipLaunchKernelGGL(rotate_weights_kernel, dim3((a.head_dim + kJoinElements - 1) / kJoinElements, 2), dim3(kJoinLanes), 0, s,
+                     a, static_cast<int>(groups_of(a, kRotateGroups)));
   return hipGetLastError();
 }
 
