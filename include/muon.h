@@ -465,7 +465,8 @@ muon_status_t muon_window_attention_backward(const muon_attention_grad_t* args, 
  *   z_l = y_l cos u - y_h sin u,  z_h = y_h cos u + y_l sin u
  *   z_d = y_d for d >= rotary_dim
  * Float32 throughout, z rounded to bfloat16 once.  Angles are exact modulo a
- * turn up to 2^-65 turns a position (far positions stay as good as near ones).
+ * turn up to 2^-64 turns a position where |frequency| < 1 (far positions stay as
+ * good as near ones).
  * A token has one position per axis (time, height, width of a video, say), and
  * each pair goes by one axis.
  *   rotary.rotary_dim   a multiple of 8, 0 (no rotation) .. head_dim

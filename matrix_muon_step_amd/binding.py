@@ -313,10 +313,10 @@ def lib() -> ctypes.CDLL:
                 L.muon_grad_norm_workspace_bytes.restype = ctypes.c_size_t
                 L.muon_grad_norm_workspace_bytes.argtypes = []
                 L.muon_grad_norm.restype = ctypes.c_int
-                L.muon_grad_norm.argtypes = [P(muon_gradient_t), ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                L.muon_grad_norm.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_size_t, ctypes.c_void_p]
                 L.muon_grad_clip.restype = ctypes.c_int
-                L.muon_grad_clip.argtypes = [P(muon_gradient_t), ctypes.c_int64, ctypes.c_double, ctypes.c_void_p,
+                L.muon_grad_clip.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_double, ctypes.c_void_p,
                                              ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
                 L.muon_copy_probe.restype = ctypes.c_int
                 L.muon_copy_probe.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32,
@@ -903,6 +903,18 @@ def _window(window, sinks):
     return _int64(window, "window"), sinks
 
 
+def _new_pair(q, k, tokens):
+    """Outputs of the shapes of q and k, (rows, heads, head_dim) each, as views of one
+    buffer, with zeros in the rows that the call leaves alone, and their muon_heads_t."""
+    rows, heads, dim = q.shape
+    both = heads + k.shape[1]
+    t = q.new_empty((rows, both, dim))
+    if rows > tokens:
+        t[tokens:].zero_()
+    at, token = t.data_ptr(), both * dim
+    return (*t.split((heads, both - heads), 1), muon_heads_t(at, token, dim), muon_heads_t(at + 2 * heads * dim, token, dim))
+
+
 def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, max_logit=None, stream=None, window=None,
                    sinks=0):
     """Causal self-attention of packed sequences; returns (o, lse).
@@ -1110,8 +1122,8 @@ def muon_qk_norm_rotate(q, k, packing: MuonPacking, rotary: Optional[MuonRotary]
     taken as they are.  positions: int32 or int64, (tokens) or (axes, tokens);
     default: each token's index in its sequence, on every axis.  q_out may be q
     and k_out k.  Outputs given by the caller keep what they hold in rows behind
-    the last sequence, outputs made here hold zeros there.  stream: as for
-    muon_attention."""
+    the last sequence; outputs made here are views of one buffer and hold zeros
+    there.  stream: as for muon_attention."""
     rows = q.shape[0]
     vq, device = _heads_tensor("q", q, rows, None)
     vk, device = _heads_tensor("k", k, rows, device)
@@ -1122,9 +1134,11 @@ def muon_qk_norm_rotate(q, k, packing: MuonPacking, rotary: Optional[MuonRotary]
     made = [v or muon_heads_t() for v in views]
     args, device = _rotate_args(q, k, packing, rotary, positions, norm, q_weight, k_weight, eps, made, device)
     with _on(device, stream) as st:
-        if q_out is None:
+        if q_out is None and k_out is None:
+            q_out, k_out, args.q_out, args.k_out = _new_pair(q, k, packing.tokens)
+        elif q_out is None:
             q_out, args.q_out = _new_heads(q, packing.tokens)
-        if k_out is None:
+        elif k_out is None:
             k_out, args.k_out = _new_heads(k, packing.tokens)
         _check(lib().muon_qk_norm_rotate(ctypes.byref(args), packing._enter(device, st), ctypes.c_void_p(st.cuda_stream)))
     return q_out, k_out
@@ -1170,9 +1184,11 @@ def muon_qk_norm_rotate_backward(d_q_out, d_k_out, q, k, packing: MuonPacking, r
             raise ValueError(f"{name} without the weight")
         device = _rotate_weight(name, d, args.head_dim, device)[1]
     with _on(device, stream) as st:
-        if dq is None:
+        if dq is None and dk is None:
+            dq, dk, args.q_out, args.k_out = _new_pair(d_q_out, d_k_out, packing.tokens)
+        elif dq is None:
             dq, args.q_out = _new_heads(d_q_out, packing.tokens)
-        if dk is None:
+        elif dk is None:
             dk, args.k_out = _new_heads(d_k_out, packing.tokens)
         if q_weight is not None and d_q_weight is None:
             d_q_weight = torch.empty_like(q_weight)
@@ -1363,19 +1379,25 @@ def muon_checkpoint_grad(matrices, accumulate=False, workspace=None, stream=None
 
 
 def _gradient_items(gradients, outs):
-    arr = (muon_gradient_t * max(1, len(gradients)))()
-    device = None
+    """The call's muon_gradient_t array, as 64-bit words (its two 32-bit types in one)."""
+    import torch
+
+    f32, bf16 = torch.float32, torch.bfloat16
+    words, device = [], None
     for k, g in enumerate(gradients):
         out = g if outs is None else outs[k]
-        for name, t in (("g", g), ("out", out)):
+        for name, t in (("g", g), ("out", out)) if out is not g else (("g", g),):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"gradient {k}: {name} must be a contiguous GPU tensor")
-            device = _same_device(device, t, f"gradient {k}: {name}")
-        if out.shape != g.shape:
+            if t.dtype != f32 and t.dtype != bf16:
+                raise ValueError(f"gradient {k}: {name} must be float32 or bfloat16")
+            if t.device != device:
+                device = _same_device(device, t, f"gradient {k}: {name}")
+        if out is not g and out.shape != g.shape:
             raise ValueError(f"gradient {k}: out is {tuple(out.shape)}, the gradient {tuple(g.shape)}")
-        arr[k] = muon_gradient_t(g.data_ptr(), out.data_ptr(), g.numel(), _dtype_code(g, f"gradient {k}"),
-                                 _dtype_code(out, f"gradient {k}: out"))
-    return arr, device
+        words += (g.data_ptr(), out.data_ptr(), g.numel(),
+                  (MUON_F32 if g.dtype == f32 else MUON_BF16) | (MUON_F32 if out.dtype == f32 else MUON_BF16) << 32)
+    return (ctypes.c_int64 * max(4, len(words)))(*words), device
 
 
 def _norm_tensor(norm, device):
@@ -1386,8 +1408,15 @@ def _norm_tensor(norm, device):
     return _same_device(device, norm, "norm")
 
 
+_norm_bytes = 0
+
+
 def muon_grad_norm_workspace_bytes() -> int:
-    return int(lib().muon_grad_norm_workspace_bytes())
+    """Bytes of the workspace of muon_grad_norm and muon_grad_clip (one size for every call)."""
+    global _norm_bytes
+    if not _norm_bytes:
+        _norm_bytes = int(lib().muon_grad_norm_workspace_bytes())
+    return _norm_bytes
 
 
 def muon_grad_norm(gradients, norm=None, workspace=None, stream=None):

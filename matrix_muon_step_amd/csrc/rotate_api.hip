@@ -40,12 +40,13 @@ bool same_view(const muon_heads_t& a, const muon_heads_t& b) {
 }
 
 // Turns per position times 2^64, modulo 2^64: whole turns fall out.  In 80
-// bits: rounded by at most 2^-65 turns where |f| < 1.
+// bits (64 of them significant): off by at most 2^-64 turns where |f| < 1.
 uint64_t turns_of(double frequency) {
-  long double t = static_cast<long double>(frequency) / 6.283185307179586476925286766559005768L;
-  t -= floorl(t);
-  t = ldexpl(t, 64);  // 0 .. 2^64
-  return t >= 18446744073709551615.0L ? 0 : static_cast<uint64_t>(t + 0.5L);
+  long double t = static_cast<long double>(fabs(frequency)) * 0.159154943091895335768883763372514362L;  // 1 / 2 pi
+  t -= static_cast<long double>(static_cast<int64_t>(t));
+  t *= 0x1p64L;
+  const uint64_t u = t + 0.5L < 0x1p64L ? static_cast<uint64_t>(t + 0.5L) : 0;
+  return frequency < 0 ? 0 - u : u;
 }
 
 muon_status_t check(const Call& c, muon_packing_t packing, const std::vector<Range>& more) {

@@ -12,7 +12,7 @@
 //
 // Angles: a frequency is held as turns per position times 2^64; its product
 // with the position modulo 2^64 is the angle modulo one turn, exact but for the
-// frequency's own rounding (2^-65 turns a position), however far the position.
+// frequency's own rounding (2^-64 turns a position), however far the position.
 // Sine and cosine of what is left of it next to a quarter turn by their power series.
 //
 // Bound by memory: each element is read and written once.  A lane holds 8 (or
@@ -388,9 +388,9 @@ __global__ __launch_bounds__(kRotateLanes, 4) void rotate_backward_kernel(const 
   }
 }
 
-// The weights' gradients from the work-groups' sums, in float64: 16 elements
-// of one tensor to a work-group, 64 lanes to four of them.
-constexpr int kJoinLanes = 256, kJoinElements = 16;
+// The weights' gradients from the work-groups' sums, in float64: 8 elements
+// of one tensor to a work-group, 128 lanes to four of them.
+constexpr int kJoinLanes = 256, kJoinElements = 8;
 __global__ __launch_bounds__(kJoinLanes) void rotate_weights_kernel(const RotateArgs a, int groups) {
   constexpr int R = kJoinLanes / (kJoinElements / 4);
   __shared__ double part[R][kJoinElements + 1];
