@@ -444,10 +444,9 @@ muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_pa
  *           hides no key of the packing gives muon_attention's bits
  *   sinks   0 .. MUON_MAX_SINKS first rows of each sequence
  * max_logit is over visible pairs.  A NaN or infinity in a sequence may reach
- * rows of it that do not see it, as there.  The backward workspace
- * holds, beside muon_attention_backward's, 8 * head_dim * kv_heads * sinks
- * bytes for every 1024 rows of a sequence, times 4 for up to 32 sinks and 2 for
- * up to 64. */
+ * rows of it that do not see it, as there.  The backward workspace holds,
+ * beside muon_attention_backward's, 8 * head_dim * kv_heads * sinks bytes for
+ * every 256 rows (or fewer) of a sequence, where the window hides any. */
 #define MUON_MAX_SINKS 128
 muon_status_t muon_window_attention(const muon_attention_t* args, int64_t window, int64_t sinks, muon_packing_t packing,
                                     void* stream);

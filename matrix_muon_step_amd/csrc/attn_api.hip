@@ -109,12 +109,8 @@ bool set_window(AttnArgs& a, const Window* w, muon_packing_t p) {
 
 int64_t row_stride(muon_packing_t p) { return round_up(std::max<int64_t>(p->tokens, 1), 64); }
 
-// Sums for the first tokens that one chunk and key head leaves: the waves that
-// share a 32-key block of them.
-int32_t far_parts(const Window* w, muon_packing_t p) {
-  if (!hides(w, p) || w->sinks == 0) return 0;
-  return w->sinks <= 32 ? 4 : w->sinks <= 64 ? 2 : 1;
-}
+// Whether the backward pass sums over rows beyond their windows.
+bool has_far(const Window* w, muon_packing_t p) { return hides(w, p) && w->sinks > 0; }
 
 size_t row_bytes(int32_t heads, muon_packing_t p) {
   return align_up(static_cast<size_t>(row_stride(p)) * heads * 2 * sizeof(float));
@@ -122,8 +118,8 @@ size_t row_bytes(int32_t heads, muon_packing_t p) {
 
 size_t backward_bytes(const muon_attention_grad_t& g, const Window* w, muon_packing_t p) {
   size_t bytes = row_bytes(g.heads, p);
-  if (const int32_t parts = far_parts(w, p))
-    bytes += align_up(static_cast<size_t>(p->chunks) * g.kv_heads * parts * 2 * static_cast<size_t>(w->sinks) * g.head_dim *
+  if (has_far(w, p))
+    bytes += align_up(static_cast<size_t>(p->chunks) * g.kv_heads * 2 * static_cast<size_t>(w->sinks) * g.head_dim *
                       sizeof(float));
   return bytes;
 }
@@ -303,8 +299,10 @@ muon_status_t attention_backward(const muon_attention_grad_t* args, const Window
   a.by_key = packing->by_key;
   a.n_tiles = static_cast<int32_t>(packing->n_tiles);
   const bool windowed = set_window(a, w, packing);
-  a.far_parts = far_parts(w, packing);
-  a.far = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + row_bytes(g.heads, packing));
+  if (has_far(w, packing)) {
+    a.far = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + row_bytes(g.heads, packing));
+    a.far_joined = (packing->longest + kFarRows - 1) / kFarRows - w->window / kFarRows > kFarDirect;
+  }
   const hipError_t e =
       (windowed ? launch_window_attention_backward : launch_attention_backward)(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MUON_OK : hip_fail(e, "attention backward launch");

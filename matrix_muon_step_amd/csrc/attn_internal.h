@@ -14,7 +14,10 @@ constexpr int kAttnStep = 64;
 constexpr int kAttnMaxDim = 128;
 // Rows of a sequence that one work item of the first tokens' gradients sums
 // over (a multiple of kAttnRows).
-constexpr int kFarRows = 1024;
+constexpr int kFarRows = 256;
+// Chunks of a sequence that the dK/dV kernel adds itself; more are joined by a
+// launch of their own first.
+constexpr int kFarDirect = 8;
 constexpr float kAttnLog2e = 1.44269504088896340736f;
 
 // One work item of a packing: rows first .. first + min(kAttnRows, len -
@@ -51,8 +54,8 @@ struct AttnArgs {
   int32_t longest;             // most keys that a row's work item visits: tokens of the longest sequence, or fewer
   // windowed calls only
   int32_t window, sinks;       // row i sees key j <= i where i - j < window or j < sinks
-  int32_t far_parts;           // backward: sums of a chunk's rows beyond their windows (0: there are none)
-  float* far;                  // backward workspace: those sums
+  float* far;                  // backward workspace: sums over rows beyond their windows (NULL: there are none)
+  int32_t far_joined;          // the first chunk's sums are a sequence's
 };
 
 hipError_t launch_attention(const AttnArgs& a, hipStream_t s);

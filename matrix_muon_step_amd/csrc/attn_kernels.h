@@ -328,32 +328,20 @@ struct KeyStream {
   }
 };
 
-// Whether no row of a wave's 32 from wq0 on sees a key of the tile from k0 on.
+// Whether no row of a wave's 32 from wq0 on sees one of the n keys from k0 on.
 template <bool WIN>
-__device__ __forceinline__ bool tile_hidden(const AttnArgs& a, int wq0, int k0) {
-  return k0 > wq0 + 31 || (WIN && wq0 - (k0 + kAttnStep - 1) >= a.window && k0 >= a.sinks);
+__device__ __forceinline__ bool keys_hidden(const AttnArgs& a, int wq0, int k0, int n) {
+  return k0 > wq0 + 31 || (WIN && wq0 - (k0 + n - 1) >= a.window && k0 >= a.sinks);
 }
 // Whether every row of the 32 from wq0 on sees every one of the n keys from k0 on.
 template <bool WIN>
 __device__ __forceinline__ bool all_seen(const AttnArgs& a, int wq0, int k0, int n) {
   return k0 + n - 1 <= wq0 && (!WIN || wq0 + 31 - k0 < a.window);
 }
-// -infinity in place of the scores of keys k0 + res_row(r) that row q does not see.
+// Whether row q does not see the key; `first`: min(sinks, q + 1).
 template <bool WIN>
-__device__ __forceinline__ void hide(const AttnArgs& a, int q, int k0, int h, f32x16_t& s) {
-  if (!WIN) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-      if (k0 + res_row(r, h) > q) s[r] = -kInf;
-    return;
-  }
-  // q - key in 0 .. window - 1, or else a key below `first`
-  const int first = min(a.sinks, q + 1);
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int key = k0 + res_row(r, h);
-    if (static_cast<uint32_t>(q - key) >= static_cast<uint32_t>(a.window) && key >= first) s[r] = -kInf;
-  }
+__device__ __forceinline__ bool key_hidden(const AttnArgs& a, int q, int key, int first) {
+  return WIN ? static_cast<uint32_t>(q - key) >= static_cast<uint32_t>(a.window) && key >= first : key > q;
 }
 
 // Hands a wave's accumulators over through LDS, 1 KB per four registers.
@@ -405,7 +393,7 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
   const int kv = hx % a.kv_heads;
   const int head = kv * (a.heads / a.kv_heads) + hx / a.kv_heads;
   const int wq0 = t.first + 32 * (wave & 3);   // the wave's first query row in its sequence
-  const int q = wq0 + (lane & 31);
+  const int q = wq0 + (lane & 31), first = WIN ? min(a.sinks, q + 1) : 0;
   const float c = a.scale * kAttnLog2e;
   const float slack = kSlackLog2 / c;
 
@@ -425,7 +413,7 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
     const int k0 = stream.key_of(it * SPLIT + part), cur = stream.fill ^ KS::TURN;
     next_tile();
     if (it + 1 < turns) stream.next(lds, wave);
-    if (tile_hidden<WIN>(a, wq0, k0) || wq0 >= t.len) continue;  // no key for the wave's rows, or it has none
+    if (keys_hidden<WIN>(a, wq0, k0, kAttnStep) || wq0 >= t.len) continue;  // no key for the wave's rows, or it has none
     const LAS unsigned char* kt_lds = lds + cur;
     const LAS unsigned char* vt_lds = kt_lds + G::TILEB;
     f32x16_t s[2];
@@ -437,7 +425,10 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
     }
     if (!all_seen<WIN>(a, wq0, k0, kAttnStep)) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) hide<WIN>(a, q, k0 + 32 * b, h, s[b]);
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (key_hidden<WIN>(a, q, k0 + 32 * b + res_row(r, h), first)) s[b][r] = -kInf;
     }
     float top = s[0][0];
 #pragma unroll
@@ -542,7 +533,7 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 && SPLIT == 1 ? 4 : 2) void a
   const int kv = hx % a.kv_heads;
   const int head = kv * (a.heads / a.kv_heads) + hx / a.kv_heads;
   const int wq0 = t.first + 32 * (wave & 3);
-  const int q = wq0 + (lane & 31);
+  const int q = wq0 + (lane & 31), first = WIN ? min(a.sinks, q + 1) : 0;
   const bool live = q < t.len;
   const int64_t row = static_cast<int64_t>(t.row0) + q;
   const float c = a.scale * kAttnLog2e;
@@ -578,17 +569,22 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 && SPLIT == 1 ? 4 : 2) void a
     const int k0 = stream.key_of(it * SPLIT + part), cur = stream.fill ^ KS::TURN;
     next_tile();
     if (it + 1 < turns) stream.next(lds, wave);
-    if (tile_hidden<WIN>(a, wq0, k0) || wq0 >= t.len) continue;
+    if (keys_hidden<WIN>(a, wq0, k0, kAttnStep) || wq0 >= t.len) continue;
     const LAS unsigned char* kt_lds = lds + cur;
     const LAS unsigned char* vt_lds = kt_lds + G::TILEB;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
+      if (WIN && keys_hidden<WIN>(a, wq0, k0 + 32 * b, 32)) continue;
       f32x16_t s = (f32x16_t)(0.f), dp = (f32x16_t)(0.f);
 #pragma unroll
       for (int st = 0; st < G::KS; ++st) s = mfma(row_frag<DP>(kt_lds, fo, b, st), qf[st], s);
 #pragma unroll
       for (int st = 0; st < G::KS; ++st) dp = mfma(row_frag<DP>(vt_lds, fo, b, st), gf[st], dp);
-      if (!all_seen<WIN>(a, wq0, k0 + 32 * b, 32)) hide<WIN>(a, q, k0 + 32 * b, h, s);
+      if (!all_seen<WIN>(a, wq0, k0 + 32 * b, 32)) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (key_hidden<WIN>(a, q, k0 + 32 * b + res_row(r, h), first)) s[r] = -kInf;
+      }
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
 #pragma unroll
@@ -633,11 +629,10 @@ struct DkvLds {
   static constexpr int BYTES = MSG + 2 * 8 * 2048;
 };
 
-// Where the far kernel's sums of chunk `slot`, key head kv and wave part lie:
-// dK (which = 0) or dV (1) of the first tokens, sinks x head_dim.
-__device__ __forceinline__ float* far_sum(const AttnArgs& a, int slot, int kv, int part, int which) {
-  const int64_t i = ((static_cast<int64_t>(slot) * a.kv_heads + kv) * a.far_parts + part) * 2 + which;
-  return a.far + i * (a.sinks * a.head_dim);
+// Where the far kernel's sums of chunk `slot` and key head kv lie: dK and dV
+// of the first tokens, 2 x sinks x head_dim.
+__device__ __forceinline__ float* far_sum(const AttnArgs& a, int slot, int kv) {
+  return a.far + (static_cast<int64_t>(slot) * a.kv_heads + kv) * (2 * a.sinks * a.head_dim);
 }
 
 // Four consecutive per-row values of a tile.
@@ -718,7 +713,13 @@ __device__ __forceinline__ bool unseen(const AttnArgs& a, int q, int key) {
   return WIN ? static_cast<uint32_t>(q - key) >= static_cast<uint32_t>(a.window) : key > q;
 }
 
-template <int DP, bool EXACT, int NW>
+//
+// With a window, key tiles next to each other want overlapping ranges of
+// rows.  They all start where the row tile's number is the same modulo the
+// range's tiles and wrap round at its end, so that work-groups that run
+// together read the same tiles at about the same time (16384 tokens, window
+// 1024, 32 heads of 128 over 8 key heads: dK/dV 582 us, 644 without).
+template <int DP, bool EXACT, int NW, bool WIN>
 struct QueryStream {
   using L = DkvLds<DP>;
   TileLoad<DP, EXACT, NW> ql, gl;
@@ -726,14 +727,22 @@ struct QueryStream {
   int64_t stat_stride;
   int64_t q_head, q_back, g_head, g_back;  // bytes to the next head; from the last head to the first, a tile back
   int row, head, group;        // first row and head of the next tile
+  int wrap;                    // WIN only: rows from the range's first tile to behind its last
   int fill;                    // its place in LDS
+  // Number, in the range, of the tile to start with.
+  static __device__ __forceinline__ int start(const AttnArgs& a, const AttnTile& t, int nq) {
+    if (!WIN) return nq - 1;
+    const int range = (kAttnRows - 1 + a.window + kAttnStep - 1) / kAttnStep;
+    return min(range - 1 - t.first / kAttnStep % range, nq - 1);
+  }
   __device__ __forceinline__ QueryStream(const AttnArgs& a, const AttnTile& t, int kv, int nq, int wave, int lane)
-      : ql(a.q, t.row0 + static_cast<int64_t>(t.first) + (nq - 1) * kAttnStep, kv * (a.heads / a.kv_heads), a.head_dim, wave,
-           lane),
-        gl(a.d_o, t.row0 + static_cast<int64_t>(t.first) + (nq - 1) * kAttnStep, kv * (a.heads / a.kv_heads), a.head_dim,
-           wave, lane) {
+      : ql(a.q, t.row0 + static_cast<int64_t>(t.first) + start(a, t, nq) * kAttnStep, kv * (a.heads / a.kv_heads), a.head_dim,
+           wave, lane),
+        gl(a.d_o, t.row0 + static_cast<int64_t>(t.first) + start(a, t, nq) * kAttnStep, kv * (a.heads / a.kv_heads),
+           a.head_dim, wave, lane) {
     group = a.heads / a.kv_heads;
-    row = t.first + (nq - 1) * kAttnStep;
+    row = t.first + start(a, t, nq) * kAttnStep;
+    if (WIN) wrap = nq * kAttnStep;
     head = fill = 0;
     stat = (wave == 0 ? a.row_lse2 : a.row_delta) + kv * group * a.row_stride + t.row0 + row;
     stat_stride = a.row_stride;
@@ -742,9 +751,9 @@ struct QueryStream {
     q_back = -((group - 1) * a.q.hs + kAttnStep * a.q.ts) * 2;
     g_back = -((group - 1) * a.d_o.hs + kAttnStep * a.d_o.ts) * 2;
   }
-  // Starts this wave's loads of the next of RING tiles.
+  // Starts this wave's loads of the next of RING tiles; `first`: the range's first row.
   template <int RING>
-  __device__ __forceinline__ void next(int len, LAS unsigned char* lds, int wave) {
+  __device__ __forceinline__ void next(int len, int first, LAS unsigned char* lds, int wave) {
     LAS unsigned char* dst = lds + fill;
     ql.load(len - row, dst, wave);
     gl.load(len - row, dst + Geo<DP>::TILEB, wave);
@@ -758,6 +767,12 @@ struct QueryStream {
       ql.move(q_back);
       gl.move(g_back);
       stat -= (group - 1) * stat_stride + kAttnStep;
+      if (WIN && row < first) {
+        row += wrap;
+        ql.move(static_cast<int64_t>(ql.ts2) * wrap);
+        gl.move(static_cast<int64_t>(gl.ts2) * wrap);
+        stat += wrap;
+      }
     } else {
       ql.move(q_head);
       gl.move(g_head);
@@ -767,25 +782,26 @@ struct QueryStream {
 };
 
 // What rows beyond their windows give the first tokens' dK (which = 0) or dV
-// (1): the far kernel's partial sums of the sequence, added in order.
+// (1): the far kernel's sums of the sequence's chunks, in order (or in the
+// first of them, joined).
 template <int DP>
 __device__ __forceinline__ void add_far(const AttnArgs& a, const AttnTile& t, int kv, int key, int which, int h,
                                         f32x16_t (&acc)[Geo<DP>::DB]) {
-  if (!a.far_parts || key >= a.sinks || t.len <= a.window) return;
-  for (int c = a.window / kFarRows; c * kFarRows < t.len; ++c)
-    for (int part = 0; part < a.far_parts; ++part) {
-      const float* p = far_sum(a, t.chunk + c, kv, part, which) + key * a.head_dim;
+  if (!a.far || key >= a.sinks || t.len <= a.window) return;
+  const int first = a.window / kFarRows, end = a.far_joined ? first + 1 : (t.len + kFarRows - 1) / kFarRows;
+  for (int c = first; c < end; ++c) {
+    const float* p = far_sum(a, t.chunk + c, kv) + (which * a.sinks + key) * a.head_dim;
 #pragma unroll
-      for (int db = 0; db < Geo<DP>::DB; ++db)
+    for (int db = 0; db < Geo<DP>::DB; ++db)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int d = 32 * db + 8 * g + 4 * h;
-          if (d >= a.head_dim) continue;
-          const f32x4_t x = gld<f32x4_t>(p + d);
+      for (int g = 0; g < 4; ++g) {
+        const int d = 32 * db + 8 * g + 4 * h;
+        if (d >= a.head_dim) continue;
+        const f32x4_t x = gld<f32x4_t>(p + d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[db][4 * g + i] += x[i];
-        }
-    }
+        for (int i = 0; i < 4; ++i) acc[db][4 * g + i] += x[i];
+      }
+  }
 }
 
 template <int DP, bool EXACT, bool WIN>
@@ -806,7 +822,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
   const float c = a.scale * kAttnLog2e;
 
   const FragOff fo = frag_offsets(lane);
-  QueryStream<DP, EXACT, 8> stream(a, t, kv, nq, wave, lane);
+  QueryStream<DP, EXACT, 8, WIN> stream(a, t, kv, nq, wave, lane);
   const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
   bf16x8_t kf[G::KS], vf[G::KS];
   own_rows<DP>(a.k.p + (krow0 * a.k.ts + kv * a.k.hs) * 2, a.k.ts, a.head_dim, t.len - wk0, lane, kf);
@@ -829,6 +845,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
     if (++head == group) {
       head = 0;
       qs -= kAttnStep;
+      if (WIN && qs < t.first) qs += stream.wrap;
     }
   };
   auto pass_on = [&]() {
@@ -838,16 +855,16 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
     const bf16x8_t other[2] = {half == 0 ? ds[0] : p[0], half == 0 ? ds[1] : p[1]};
     write_msg(lds + out + turn, other);
   };
-  stream.template next<3>(t.len, lds, wave);
+  stream.template next<3>(t.len, t.first, lds, wave);
   next_tile();
-  if (total > 1) stream.template next<3>(t.len, lds, wave);
+  if (total > 1) stream.template next<3>(t.len, t.first, lds, wave);
   dkv_scores<DP>(lds + cur, fo, half, kf, vf, s, dp);
   mask();
   dkv_softmax<DP>(lds + cur, half, h, c, s, dp);
   pass_on();
   for (int it = 1; it < total; ++it) {
     next_tile();  // tile `it` and the messages of turn it - 1 are there, tile it - 2 is done with
-    if (it + 1 < total) stream.template next<3>(t.len, lds, wave);
+    if (it + 1 < total) stream.template next<3>(t.len, t.first, lds, wave);
     const int prev = cur + sum_of;
     cur = cur == 2 * L::STAGE ? 0 : cur + L::STAGE;
     turn ^= 8 * 2048;
@@ -893,9 +910,9 @@ __global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a)
   const int key = wk0 + (lane & 31);
   const float c = a.scale * kAttnLog2e;
   const FragOff fo = frag_offsets(lane);
-  QueryStream<DP, EXACT, 4> stream(a, t, kv, nq, wave, lane);
+  QueryStream<DP, EXACT, 4, WIN> stream(a, t, kv, nq, wave, lane);
   int q0 = stream.row, head = 0, cur = 0;
-  stream.template next<2>(t.len, lds, wave);
+  stream.template next<2>(t.len, t.first, lds, wave);
   const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
   bf16x8_t kf[G::KS], vf[G::KS];
   own_rows<DP>(a.k.p + (krow0 * a.k.ts + kv * a.k.hs) * 2, a.k.ts, a.head_dim, t.len - wk0, lane, kf);
@@ -905,7 +922,7 @@ __global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a)
   for (int db = 0; db < G::DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
   for (int it = 0; it < total; ++it) {
     next_tile();
-    if (it + 1 < total) stream.template next<2>(t.len, lds, wave);
+    if (it + 1 < total) stream.template next<2>(t.len, t.first, lds, wave);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int qs = q0 + 32 * b;
@@ -927,6 +944,7 @@ __global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a)
     if (++head == stream.group) {
       head = 0;
       q0 -= kAttnStep;
+      if (WIN && q0 < t.first) q0 += stream.wrap;
     }
   }
   if (WIN) {

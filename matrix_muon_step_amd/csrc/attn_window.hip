@@ -14,11 +14,12 @@ namespace {
 // and no atomics.  Rows stream past as in the dK/dV kernels.  The 4 waves
 // share out 32-key blocks of the first tokens, and what is left over, the rows:
 // with up to 32 of them each wave takes a 32-row half of every other tile, with
-// up to 64 one half of every tile.
+// up to 64 one half of every tile.  Bound by the reads of q and dO.
 template <int DP, bool EXACT>
 __global__ __launch_bounds__(256, 2) void attention_far_kernel(const AttnArgs a) {
   using G = Geo<DP>;
   using L = DkvLds<DP>;
+  static_assert(2 * L::STAGE >= 4 * 32 * DP * 4, "the waves' sums fit the buffer");
   __shared__ __align__(1024) unsigned char smem[2 * L::STAGE];
   LAS unsigned char* lds = (LAS unsigned char*)smem;
   const int lane = threadIdx.x & 63, h = lane >> 5;
@@ -31,13 +32,14 @@ __global__ __launch_bounds__(256, 2) void attention_far_kernel(const AttnArgs a)
   rows.first = max(t.first, a.window / kAttnStep * kAttnStep);
   const int nq = (end - rows.first + kAttnStep - 1) / kAttnStep;
   const int total = nq * (a.heads / a.kv_heads);
-  const int part = wave % a.far_parts, wk0 = wave / a.far_parts * 32;
+  const int parts = a.sinks <= 32 ? 4 : a.sinks <= 64 ? 2 : 1;  // waves that share a key block
+  const int part = wave % parts, wk0 = wave / parts * 32;
   const int key = wk0 + (lane & 31);
   const float c = a.scale * kAttnLog2e;
   const FragOff fo = frag_offsets(lane);
-  QueryStream<DP, EXACT, 4> stream(a, rows, kv, nq, wave, lane);
+  QueryStream<DP, EXACT, 4, false> stream(a, rows, kv, nq, wave, lane);
   int q0 = stream.row, head = 0, cur = 0;
-  stream.template next<2>(t.len, lds, wave);
+  stream.template next<2>(t.len, 0, lds, wave);
   const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
   const int keys = min(t.len, a.sinks) - wk0;
   bf16x8_t kf[G::KS], vf[G::KS];
@@ -48,12 +50,12 @@ __global__ __launch_bounds__(256, 2) void attention_far_kernel(const AttnArgs a)
   for (int db = 0; db < G::DB; ++db) dk[db] = dv[db] = (f32x16_t)(0.f);
   for (int it = 0; it < total; ++it) {
     next_tile();
-    if (it + 1 < total) stream.template next<2>(t.len, lds, wave);
+    if (it + 1 < total) stream.template next<2>(t.len, 0, lds, wave);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int qs = q0 + 32 * b;
-      if (a.far_parts > 1 && b != (part & 1)) continue;             // another wave's half
-      if (a.far_parts > 2 && (it & 1) != (part >> 1)) continue;     // or tile
+      if (parts > 1 && b != (part & 1)) continue;             // another wave's half
+      if (parts > 2 && (it & 1) != (part >> 1)) continue;     // or tile
       if (keys <= 0 || qs + 31 < a.window || qs >= t.len) continue;
       f32x16_t s, dp;
       dkv_scores<DP>(lds + cur, fo, b, kf, vf, s, dp);
@@ -73,26 +75,54 @@ __global__ __launch_bounds__(256, 2) void attention_far_kernel(const AttnArgs a)
       q0 -= kAttnStep;
     }
   }
-  if (key >= a.sinks) return;
+  // The waves' sums, dK's and then dV's, through LDS: 32 keys x DP a wave.
+  float* out = far_sum(a, t.chunk + t.first / kFarRows, kv);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    float* p = far_sum(a, t.chunk + t.first / kFarRows, kv, part, which) + key * a.head_dim;
+    lds_barrier();  // the last tile, or dK's sums, are read
+    LAS unsigned char* mine = lds + (wave * 32 + (lane & 31)) * (DP * 4) + 16 * h;
 #pragma unroll
     for (int db = 0; db < G::DB; ++db)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int d = 32 * db + 8 * g + 4 * h;
         const f32x16_t& x = which ? dv[db] : dk[db];
-        if (d < a.head_dim) gst(p + d, (f32x4_t){x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]});
+        *(LAS f32x4_t*)(mine + 128 * db + 32 * g) = (f32x4_t){x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
       }
+    lds_barrier();
+    const int per_key = a.head_dim / 4;
+    for (int i = threadIdx.x; i < a.sinks * per_key; i += 256) {
+      const int row = i / per_key, d = (i - row * per_key) * 4;
+      f32x4_t sum = (f32x4_t)(0.f);
+      for (int w = 0; w < parts; ++w)
+        sum += *(const LAS f32x4_t*)(lds + (((row >> 5) * parts + w) * 32 + (row & 31)) * (DP * 4) + d * 4);
+      gst(out + (which * a.sinks + row) * a.head_dim + d, sum);
+    }
   }
+}
+
+// Joins the sums of a sequence's chunks, in order, into its first.
+__global__ __launch_bounds__(256) void attention_far_join_kernel(const AttnArgs a) {
+  const int kv = blockIdx.x % a.kv_heads;
+  const AttnTile t = a.by_query[blockIdx.x / a.kv_heads];
+  const int i = blockIdx.y * 256 + threadIdx.x;
+  if (t.first != 0 || t.len <= a.window || i >= a.sinks * a.head_dim / 2) return;
+  const int first = a.window / kFarRows, end = (t.len + kFarRows - 1) / kFarRows;
+  float* p = far_sum(a, t.chunk + first, kv) + 4 * i;
+  const int64_t step = far_sum(a, 1, 0) - far_sum(a, 0, 0);
+  f32x4_t sum = gld<f32x4_t>(p);
+#pragma unroll 8
+  for (int c = 1; c < end - first; ++c) sum += gld<f32x4_t>(p + c * step);
+  gst(p, sum);
 }
 
 template <int DP, bool EXACT>
 hipError_t far_rows(const AttnArgs& a, hipStream_t s) {
-  if (!a.far_parts) return hipSuccess;
-  hipLaunchKernelGGL((attention_far_kernel<DP, EXACT>), dim3(static_cast<uint32_t>(a.n_tiles) * a.kv_heads), dim3(256), 0, s,
-                     a);
+  if (!a.far) return hipSuccess;
+  const uint32_t grid = static_cast<uint32_t>(a.n_tiles) * a.kv_heads;
+  hipLaunchKernelGGL((attention_far_kernel<DP, EXACT>), dim3(grid), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.far_joined) return e;
+  hipLaunchKernelGGL(attention_far_join_kernel, dim3(grid, (a.sinks * a.head_dim / 2 + 255) / 256), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
