@@ -357,15 +357,29 @@ template <bool WIN>
 __device__ __forceinline__ bool keys_hidden(const AttnArgs& a, int wq0, int k0, int n) {
   return k0 > wq0 + 31 || (WIN && wq0 - (k0 + n - 1) >= a.window && k0 >= a.sinks);
 }
-// Whether every row of the 32 from wq0 on sees every one of the n keys from k0 on.
-template <bool WIN>
-__device__ __forceinline__ bool all_seen(const AttnArgs& a, int wq0, int k0, int n) {
-  return k0 + n - 1 <= wq0 && (!WIN || wq0 + 31 - k0 < a.window);
-}
-// Whether row q does not see the key; `first`: min(sinks, q + 1).
-template <bool WIN>
-__device__ __forceinline__ bool key_hidden(const AttnArgs& a, int q, int key, int first) {
-  return WIN ? static_cast<uint32_t>(q - key) >= static_cast<uint32_t>(a.window) && key >= first : key > q;
+// -infinity in place of the scores of keys k0 + res_row(r), of 32 from k0 on,
+// that row q of a wave's 32 from wq0 on does not see (windowed calls): each
+// border that the block holds costs a comparison an element.
+__device__ __forceinline__ void hide_keys(const AttnArgs& a, int wq0, int q, int k0, int h, f32x16_t& s) {
+  const int at = q - k0 - 4 * h;  // the row itself, as res_row(r, 0) counts keys
+  if (k0 + 31 > wq0) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (res_row(r, 0) > at) s[r] = -kInf;
+  }
+  if (wq0 + 31 - k0 >= a.window) {
+    const int low = at - a.window;  // the last key behind its window
+    if (k0 >= a.sinks) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (res_row(r, 0) <= low) s[r] = -kInf;
+    } else {
+      const int first = a.sinks - k0 - 4 * h;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (res_row(r, 0) <= low && res_row(r, 0) >= first) s[r] = -kInf;
+    }
+  }
 }
 
 // Hands a wave's accumulators over through LDS, 1 KB per four registers.
@@ -417,7 +431,7 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
   const int kv = hx % a.kv_heads;
   const int head = kv * (a.heads / a.kv_heads) + hx / a.kv_heads;
   const int wq0 = t.first + 32 * (wave & 3);   // the wave's first query row in its sequence
-  const int q = wq0 + (lane & 31), first = WIN ? min(a.sinks, q + 1) : 0;
+  const int q = wq0 + (lane & 31);
   const float c = a.scale * kAttnLog2e;
   const float slack = kSlackLog2 / c;
 
@@ -447,12 +461,15 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
 #pragma unroll
       for (int st = 0; st < G::KS; ++st) s[b] = mfma(row_frag<DP>(kt_lds, fo, b, st), qf[st], s[b]);
     }
-    if (!all_seen<WIN>(a, wq0, k0, kAttnStep)) {
+    if constexpr (WIN) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) hide_keys(a, wq0, q, k0 + 32 * b, h, s[b]);
+    } else if (k0 + kAttnStep - 1 > wq0) {
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (key_hidden<WIN>(a, q, k0 + 32 * b + res_row(r, h), first)) s[b][r] = -kInf;
+          if (k0 + 32 * b + res_row(r, h) > q) s[b][r] = -kInf;
     }
     float top = s[0][0];
 #pragma unroll
@@ -558,7 +575,7 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 && SPLIT == 1 ? 4 : 2) void a
   const int kv = hx % a.kv_heads;
   const int head = kv * (a.heads / a.kv_heads) + hx / a.kv_heads;
   const int wq0 = t.first + 32 * (wave & 3);
-  const int q = wq0 + (lane & 31), first = WIN ? min(a.sinks, q + 1) : 0;
+  const int q = wq0 + (lane & 31);
   const bool live = q < t.len;
   const int64_t row = static_cast<int64_t>(t.row0) + q;
   const float c = a.scale * kAttnLog2e;
@@ -605,10 +622,12 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 && SPLIT == 1 ? 4 : 2) void a
       for (int st = 0; st < G::KS; ++st) s = mfma(row_frag<DP>(kt_lds, fo, b, st), qf[st], s);
 #pragma unroll
       for (int st = 0; st < G::KS; ++st) dp = mfma(row_frag<DP>(vt_lds, fo, b, st), gf[st], dp);
-      if (!all_seen<WIN>(a, wq0, k0 + 32 * b, 32)) {
+      if constexpr (WIN) {
+        hide_keys(a, wq0, q, k0 + 32 * b, h, s);
+      } else if (k0 + 32 * b + 31 > wq0) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (key_hidden<WIN>(a, q, k0 + 32 * b + res_row(r, h), first)) s[r] = -kInf;
+          if (k0 + 32 * b + res_row(r, h) > q) s[r] = -kInf;
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
@@ -724,21 +743,23 @@ __device__ __forceinline__ int fresh_lane() {
   return l;
 }
 
-// The tiles that stream past a key tile: from the sequence's last rows back to
-// the diagonal, every query head of the group in turn, so that work-groups of
-// one key head read the same tiles at about the same time.
 // Query tiles of a key tile: from the diagonal to the last row that sees one of its keys (through its window).
 template <bool WIN>
 __device__ __forceinline__ int query_tiles(const AttnArgs& a, const AttnTile& t) {
   const int rows = t.len - t.first;
   return ((WIN ? min(rows, kAttnRows - 1 + a.window) : rows) + kAttnStep - 1) / kAttnStep;
 }
-// Whether row q does not see the key (through its window).
-template <bool WIN>
-__device__ __forceinline__ bool unseen(const AttnArgs& a, int q, int key) {
-  return WIN ? static_cast<uint32_t>(q - key) >= static_cast<uint32_t>(a.window) : key > q;
+// -infinity in place of the scores of rows q0 + res_row(r) whose windows begin behind the key.
+__device__ __forceinline__ void hide_rows(const AttnArgs& a, int q0, int key, int h, f32x16_t& s) {
+  const int last = key + a.window - 1 - q0 - 4 * h;
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+    if (res_row(r, 0) > last) s[r] = -kInf;
 }
 
+// The tiles that stream past a key tile: from the sequence's last rows back to
+// the diagonal, every query head of the group in turn, so that work-groups of
+// one key head read the same tiles at about the same time.
 //
 // With a window, key tiles next to each other want overlapping ranges of
 // rows.  They all start where the row tile's number is the same modulo the
@@ -863,11 +884,12 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
   const int out = L::MSG + wave * 2048 + lane * 16, in = L::MSG + (wave ^ 4) * 2048 + lane * 16;
   int qs = stream.row + 32 * half, head = 0;  // the wave's first row of the tile
   auto mask = [&]() {
-    if (qs < wk0 + 31 || qs + 31 >= t.len || (WIN && qs + 31 - wk0 >= a.window)) {
+    if (qs < wk0 + 31 || qs + 31 >= t.len) {
 #pragma unroll
       for (int r = 0; r < 16; ++r)
-        if (unseen<WIN>(a, qs + res_row(r, h), key) || qs + res_row(r, h) >= t.len) s[r] = -kInf;
+        if (key > qs + res_row(r, h) || qs + res_row(r, h) >= t.len) s[r] = -kInf;
     }
+    if (WIN && qs + 31 - wk0 >= a.window) hide_rows(a, qs, key, h, s);
     if (++head == group) {
       head = 0;
       qs -= kAttnStep;
@@ -956,11 +978,12 @@ __global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a)
       if (qs + 31 < wk0 || qs >= t.len || wk0 >= t.len || (WIN && qs - (wk0 + 31) >= a.window)) continue;
       f32x16_t s, dp;
       dkv_scores<DP>(lds + cur, fo, b, kf, vf, s, dp);
-      if (qs < wk0 + 31 || qs + 31 >= t.len || (WIN && qs + 31 - wk0 >= a.window)) {
+      if (qs < wk0 + 31 || qs + 31 >= t.len) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (unseen<WIN>(a, qs + res_row(r, h), key) || qs + res_row(r, h) >= t.len) s[r] = -kInf;
+          if (key > qs + res_row(r, h) || qs + res_row(r, h) >= t.len) s[r] = -kInf;
       }
+      if (WIN && qs + 31 - wk0 >= a.window) hide_rows(a, qs, key, h, s);
       dkv_softmax<DP>(lds + cur, b, h, c, s, dp);
       const bf16x8_t p[2] = {to_operand(s, 0), to_operand(s, 1)}, ds[2] = {to_operand(dp, 0), to_operand(dp, 1)};
       dkv_sums<DP>(lds + cur + G::TILEB, fo, b, p, dv);
