@@ -9,9 +9,9 @@ namespace muon {
 // Tokens of one work item, a piece of a packing's 128-row tile.
 constexpr int kRotateRows = 8;
 constexpr int kRotatePieces = kAttnRows / kRotateRows;
-// Work-groups of the backward kernel at most (four to a compute unit), each
+// Work-groups of the backward kernel at most, for each of the two tensors, each
 // with one partial sum of the weights' gradients in the workspace.
-constexpr int kRotateGroups = 1024;
+constexpr int kRotateGroups = 512;
 constexpr int kRotateLanes = 256;
 constexpr int64_t kRotateLarge = int64_t{256} << 20;
 
