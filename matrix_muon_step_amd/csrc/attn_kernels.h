@@ -1017,12 +1017,23 @@ namespace {
 // | 85 / 269; 1290 tokens, 25 of 64 (275) 20.8 / 59 | 19.3 / 55; 4 x 1024
 // tokens, 16 of 128 (512) 30 / 94 | 34 / 102; 4096 tokens, 25 of 64 (800)
 // 75 / 241 | 72 / 251.
-bool split_keys(const AttnArgs& a) { return int64_t{a.n_tiles} * a.heads <= 512 && a.longest > 1024; }
+// Windowed calls have as few turns as the window (a.longest) and end more
+// evenly: the forward pass gains up to 512 work-groups with heads of 64 (4096
+// tokens, 12 heads, window 1024: 28.5 | 25.9; window 512: 21.3 | 22.3; 8192, 8
+// heads, window 1024: 28.2 | 26.8) and 256 with heads of 128 (2048, 16 heads,
+// window 1024: 28.2 | 23.1; 4096, 16/4 heads, 512 of them: 42.7 | 47.6), the
+// backward pass up to about 300 (1290, 25 of 64: 51.9 | 48.9; 4096, 12 of 64:
+// 89 | 92).
+template <int DP, bool WIN>
+bool split_keys(const AttnArgs& a, bool back) {
+  const int64_t most = !WIN ? 512 : back ? 320 : DP == 64 ? 512 : 256;
+  return int64_t{a.n_tiles} * a.heads <= most && a.longest > 1024;
+}
 
 template <int DP, bool EXACT, bool WIN>
 hipError_t forward(const AttnArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(a.n_tiles) * a.heads);
-  if (split_keys(a)) hipLaunchKernelGGL((attention_kernel<DP, EXACT, 2, WIN>), grid, dim3(512), 0, s, a);
+  if (split_keys<DP, WIN>(a, false)) hipLaunchKernelGGL((attention_kernel<DP, EXACT, 2, WIN>), grid, dim3(512), 0, s, a);
   else hipLaunchKernelGGL((attention_kernel<DP, EXACT, 1, WIN>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
@@ -1034,7 +1045,7 @@ hipError_t far_rows(const AttnArgs& a, hipStream_t s);
 template <int DP, bool EXACT, bool WIN>
 hipError_t backward(const AttnArgs& a, hipStream_t s) {
   const dim3 rows(static_cast<uint32_t>(a.n_tiles) * a.heads);
-  if (split_keys(a)) hipLaunchKernelGGL((attention_dq_kernel<DP, EXACT, 2, WIN>), rows, dim3(512), 0, s, a);
+  if (split_keys<DP, WIN>(a, true)) hipLaunchKernelGGL((attention_dq_kernel<DP, EXACT, 2, WIN>), rows, dim3(512), 0, s, a);
   else hipLaunchKernelGGL((attention_dq_kernel<DP, EXACT, 1, WIN>), rows, dim3(256), 0, s, a);
   hipError_t e = hipGetLastError();
   if constexpr (WIN) {
@@ -1048,8 +1059,11 @@ hipError_t backward(const AttnArgs& a, hipStream_t s) {
   // us, pair | three: 1290 tokens, 25 heads (275 tiles) 53 | 60; 4096 tokens,
   // 12 heads (384) 131 | 159; 8 x 512, 16 heads (512) 41 | 37; 25 heads: 2500
   // (500) 116 | 119, 8 x 512 (800) 70 | 50, 4096 (800) 272 | 228, 64 x 64
-  // (1600) 52 | 37.
-  if (DP == 64 && grid.x > 512) hipLaunchKernelGGL((attention_dkv_kernel<64, EXACT, WIN>), grid, dim3(256), 0, s, a);
+  // (1600) 52 | 37.  With windows up to about 1100 the three-to-a-unit kernel
+  // wins from fewer on: window 512, 1290 tokens, 25 heads (275) 51.7 | 58.8; 4096,
+  // 12 heads (384) 75 | 67; window 1024, 2500, 25 heads (500) 94 | 82; window
+  // 2048, 4096, 12 heads 120 | 134.
+  if (DP == 64 && grid.x > (WIN && a.longest <= 1280 ? 320 : 512)) hipLaunchKernelGGL((attention_dkv_kernel<64, EXACT, WIN>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((attention_dkv_pair_kernel<DP, EXACT, WIN>), grid, dim3(512), 0, s, a);
   return hipGetLastError();
 }

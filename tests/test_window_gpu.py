@@ -100,6 +100,13 @@ def test_many_tiles(mm):
         check(mm, lengths, 20, 10, 40, window, sinks, behind=1)
 
 
+@pytest.mark.parametrize("dim", [64, 40])
+def test_many_tiles_of_long_sequences(mm, dim):
+    """The same with sums of the first tokens that are joined, and some that are not."""
+    check(mm, [3000, 7, 400], 14, 14, dim, 90, 4, sharp=1.0)
+    check(mm, [2600], 17, 17, dim, 300, 70, behind=1, sharp=1.0)
+
+
 def test_windows_that_hide_nothing(mm):
     """muon_attention's bits, with any number of first tokens."""
     print("[case] windows over everything", flush=True)
