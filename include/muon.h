@@ -444,12 +444,19 @@ muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_pa
  *           hides no key of the packing gives muon_attention's bits
  *   sinks   0 .. MUON_MAX_SINKS first rows of each sequence
  * max_logit is over visible pairs.  A NaN or infinity in a sequence may reach
- * rows of it that do not see it, as there.  The backward workspace holds,
+ * rows of it that do not see it, as there.  The forward workspace (DEVICE,
+ * 256-byte aligned) may be NULL; with muon_window_attention_workspace_bytes
+ * bytes (4 for each 128-row piece of a sequence and head; 0 where it makes no
+ * difference, which muon_last_error() being empty tells from an error; of
+ * args' pointers only max_logit being NULL is looked at) max_logit is raised
+ * with fewer atomics.  The backward workspace holds,
  * beside muon_attention_backward's, 8 * head_dim * kv_heads * sinks bytes for
  * every 256 rows (or fewer) of a sequence, where the window hides any. */
 #define MUON_MAX_SINKS 128
+size_t muon_window_attention_workspace_bytes(const muon_attention_t* args, int64_t window, int64_t sinks,
+                                             muon_packing_t packing);
 muon_status_t muon_window_attention(const muon_attention_t* args, int64_t window, int64_t sinks, muon_packing_t packing,
-                                    void* stream);
+                                    void* workspace, size_t workspace_bytes, void* stream);
 size_t muon_window_attention_backward_workspace_bytes(const muon_attention_grad_t* args, int64_t window, int64_t sinks,
                                                       muon_packing_t packing);
 muon_status_t muon_window_attention_backward(const muon_attention_grad_t* args, int64_t window, int64_t sinks,

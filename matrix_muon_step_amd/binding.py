@@ -294,7 +294,10 @@ def lib() -> ctypes.CDLL:
                                                    ctypes.c_size_t, ctypes.c_void_p]
                 L.muon_window_attention.restype = ctypes.c_int
                 L.muon_window_attention.argtypes = [P(muon_attention_t), ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
-                                                    ctypes.c_void_p]
+                                                    ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+                L.muon_window_attention_workspace_bytes.restype = ctypes.c_size_t
+                L.muon_window_attention_workspace_bytes.argtypes = [P(muon_attention_t), ctypes.c_int64, ctypes.c_int64,
+                                                                    ctypes.c_void_p]
                 L.muon_window_attention_backward_workspace_bytes.restype = ctypes.c_size_t
                 L.muon_window_attention_backward_workspace_bytes.argtypes = [P(muon_attention_grad_t), ctypes.c_int64,
                                                                              ctypes.c_int64, ctypes.c_void_p]
@@ -965,8 +968,15 @@ def muon_attention(q, k, v, packing: MuonPacking, scale=None, o=None, lse=None, 
         args = muon_attention_t(dq, dk, dv, do, lse.data_ptr(), lse.stride(0) if heads > 1 else rows,
                                 max_logit.data_ptr() if max_logit is not None else None, logit_heads, heads, kv_heads,
                                 head_dim, float(head_dim ** -0.5 if scale is None else scale))
-        call = lib().muon_window_attention if seen else lib().muon_attention
-        _check(call(ctypes.byref(args), *seen, packing._enter(device, st), ctypes.c_void_p(st.cuda_stream)))
+        handle = packing._enter(device, st)
+        if not seen:
+            _check(lib().muon_attention(ctypes.byref(args), handle, ctypes.c_void_p(st.cuda_stream)))
+            return o, lse
+        ws = None
+        if max_logit is not None:  # an error's 0 comes again from the call itself
+            ws = _alloc_workspace(lib().muon_window_attention_workspace_bytes(ctypes.byref(args), *seen, handle), device)
+        _check(lib().muon_window_attention(ctypes.byref(args), *seen, handle, *_ws_args(ws, device),
+                                           ctypes.c_void_p(st.cuda_stream)))
     return o, lse
 
 

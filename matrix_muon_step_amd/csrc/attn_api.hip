@@ -191,7 +191,14 @@ muon_status_t check_device(muon_packing_t packing) {
 
 namespace {
 
-muon_status_t attention(const muon_attention_t* args, const Window* w, muon_packing_t packing, void* stream) {
+// Workspace that a forward pass can use: its items' largest logits.
+size_t forward_bytes(const muon_attention_t& g, const Window* w, muon_packing_t p) {
+  const int64_t items = p->n_tiles * g.heads;
+  return g.max_logit && hides(w, p) && items >= kTopItems ? align_up(static_cast<size_t>(items) * sizeof(float)) : 0;
+}
+
+muon_status_t attention(const muon_attention_t* args, const Window* w, muon_packing_t packing, void* workspace,
+                        size_t workspace_bytes, void* stream) {
   if (!args) return fail(MUON_ERR_INVALID_ARG, "muon: args is NULL");
   const muon_attention_t& g = *args;
   muon_status_t st = check_shape(g.heads, g.kv_heads, g.head_dim, g.scale, packing);
@@ -199,6 +206,15 @@ muon_status_t attention(const muon_attention_t* args, const Window* w, muon_pack
   st = check_window(w);
   if (st != MUON_OK) return st;
   std::vector<Range> others;
+  if (workspace) {
+    const size_t need = forward_bytes(g, w, packing);
+    const uintptr_t ws = reinterpret_cast<uintptr_t>(workspace);
+    if (workspace_bytes < need)
+      return fail(MUON_ERR_WORKSPACE, "muon: the attention needs " + std::to_string(need) + " bytes of workspace, or none");
+    if (ws % kAlign) return fail(MUON_ERR_WORKSPACE, "muon: workspace must be 256-byte aligned");
+    if (need > 0) others.push_back({ws, ws + need, true, "the workspace", 0});
+    else workspace = nullptr;
+  }
   st = check_lse(g.lse, g.lse_stride, packing->tokens, g.heads, true, others);
   if (st != MUON_OK) return st;
   if (g.max_logit) {
@@ -234,6 +250,7 @@ muon_status_t attention(const muon_attention_t* args, const Window* w, muon_pack
   a.by_key = packing->by_key;
   a.n_tiles = static_cast<int32_t>(packing->n_tiles);
   const bool windowed = set_window(a, w, packing);
+  a.tops = static_cast<float*>(workspace);
   const hipError_t e = (windowed ? launch_window_attention : launch_attention)(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MUON_OK : hip_fail(e, "attention launch");
 }
@@ -385,13 +402,27 @@ muon_status_t muon_packing_destroy(muon_packing_t packing) {
 }
 
 muon_status_t muon_attention(const muon_attention_t* args, muon_packing_t packing, void* stream) {
-  return guarded([&] { return attention(args, nullptr, packing, stream); });
+  return guarded([&] { return attention(args, nullptr, packing, nullptr, 0, stream); });
+}
+
+size_t muon_window_attention_workspace_bytes(const muon_attention_t* args, int64_t window, int64_t sinks,
+                                             muon_packing_t packing) {
+  const Window w = {window, sinks};
+  size_t bytes = 0;
+  guarded([&] {
+    if (!args) return fail(MUON_ERR_INVALID_ARG, "muon: args is NULL");
+    muon_status_t st = check_shape(args->heads, args->kv_heads, args->head_dim, args->scale, packing);
+    if (st == MUON_OK) st = check_window(&w);
+    if (st == MUON_OK) bytes = forward_bytes(*args, &w, packing);
+    return st;
+  });
+  return bytes;
 }
 
 muon_status_t muon_window_attention(const muon_attention_t* args, int64_t window, int64_t sinks, muon_packing_t packing,
-                                    void* stream) {
+                                    void* workspace, size_t workspace_bytes, void* stream) {
   const Window w = {window, sinks};
-  return guarded([&] { return attention(args, &w, packing, stream); });
+  return guarded([&] { return attention(args, &w, packing, workspace, workspace_bytes, stream); });
 }
 
 size_t muon_attention_backward_workspace_bytes(const muon_attention_grad_t* args, muon_packing_t packing) {

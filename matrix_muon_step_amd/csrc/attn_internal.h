@@ -15,6 +15,14 @@ constexpr int kAttnMaxDim = 128;
 // Rows of a sequence that one work item of the first tokens' gradients sums
 // over (a multiple of kAttnRows).
 constexpr int kFarRows = 256;
+// Work items from which on a windowed call leaves their largest logits in the
+// workspace, for a launch of its own to join, instead of one atomic each
+// (which follow one another, about 15 ns each where all items end at once).
+// From -infinity, us, atomics | join: 384 items (4096 tokens, 12 heads of 64,
+// window 256) 20.0 | 20.5; 516 (5500) 20.2 | 20.6; 640 (20 heads) 29 | 23.5; 950
+// (4100 in ten sequences, 25 heads) 38 | 24.5; 2048 (16384, 16 heads, window
+// 128) 48 | 39.5; 1024 (4096, 32/8 heads of 128, window 512) 63 | 60.
+constexpr int kTopItems = 576;
 // Chunks of a sequence that the dK/dV kernel adds itself; more are joined by a
 // launch of their own first.
 constexpr int kFarDirect = 8;
@@ -56,6 +64,7 @@ struct AttnArgs {
   int32_t window, sinks;       // row i sees key j <= i where i - j < window or j < sinks
   float* far;                  // backward workspace: sums over rows beyond their windows (NULL: there are none)
   int32_t far_joined;          // the first chunk's sums are a sequence's
+  float* tops;                 // forward workspace: heads x n_tiles, each item's largest logit, or NULL
 };
 
 hipError_t launch_attention(const AttnArgs& a, hipStream_t s);

@@ -550,7 +550,8 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
       const f32x4_t x = *(const LAS f32x4_t*)lds;
 #pragma unroll
       for (int w = 1; w < 4; ++w) top = top != top || x[w] != x[w] ? __builtin_nanf("") : fmaxf(top, x[w]);
-      atomic_max_float(a.max_logit + head / a.logit_group, top);
+      if (WIN && a.tops) gst(a.tops + static_cast<int64_t>(head) * a.n_tiles + blockIdx.x / a.heads, top);
+      else atomic_max_float(a.max_logit + head / a.logit_group, top);
     }
   }
 }
@@ -1030,11 +1031,18 @@ bool split_keys(const AttnArgs& a, bool back) {
   return int64_t{a.n_tiles} * a.heads <= most && a.longest > 1024;
 }
 
+// The largest logits that a windowed call's work items left in the workspace.
+hipError_t join_tops(const AttnArgs& a, hipStream_t s);
+
 template <int DP, bool EXACT, bool WIN>
 hipError_t forward(const AttnArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(a.n_tiles) * a.heads);
   if (split_keys<DP, WIN>(a, false)) hipLaunchKernelGGL((attention_kernel<DP, EXACT, 2, WIN>), grid, dim3(512), 0, s, a);
   else hipLaunchKernelGGL((attention_kernel<DP, EXACT, 1, WIN>), grid, dim3(256), 0, s, a);
+  if constexpr (WIN) {
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? join_tops(a, s) : e;
+  }
   return hipGetLastError();
 }
 

@@ -128,6 +128,30 @@ __global__ __launch_bounds__(256) void attention_far_join_kernel(const AttnArgs 
   gst(p, ((sum + part[64 + lane]) + part[128 + lane]) + part[192 + lane]);
 }
 
+// An entry's largest logit over the items of its heads, which lie together.
+__global__ __launch_bounds__(256) void attention_tops_kernel(const AttnArgs a) {
+  __shared__ float part[4];
+  const int n = a.logit_group * a.n_tiles;
+  const float* p = a.tops + static_cast<int64_t>(blockIdx.x) * n;
+  float top = -kInf;
+  auto take = [&](float x) { top = top != top || x != x ? __builtin_nanf("") : fmaxf(top, x); };
+  for (int i = threadIdx.x; i < n; i += 256) take(gld<float>(p + i));
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) take(__shfl_xor(top, off, 64));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) take(part[w]);
+  atomic_max_float(a.max_logit + blockIdx.x, top);
+}
+
+hipError_t join_tops(const AttnArgs& a, hipStream_t s) {
+  if (!a.tops) return hipSuccess;
+  hipLaunchKernelGGL(attention_tops_kernel, dim3(a.heads / a.logit_group), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
 template <int DP, bool EXACT>
 hipError_t far_rows(const AttnArgs& a, hipStream_t s) {
   if (!a.far) return hipSuccess;

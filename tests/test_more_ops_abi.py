@@ -241,8 +241,13 @@ def attention_grad(heads=4, kv=2, dim=64):
     return g
 
 
-def call_window(a, window=10, sinks=4, p=None):
-    return mm.lib().muon_window_attention(ctypes.byref(a), window, sinks, ctypes.byref(p or packing()), None)
+def call_window(a, window=10, sinks=4, p=None, ws=0, ws_bytes=0):
+    return mm.lib().muon_window_attention(ctypes.byref(a), window, sinks, ctypes.byref(p or packing()), ctypes.c_void_p(ws),
+                                          ws_bytes, None)
+
+
+def forward_bytes(a, window=10, sinks=4, p=None):
+    return mm.lib().muon_window_attention_workspace_bytes(ctypes.byref(a), window, sinks, ctypes.byref(p or packing()))
 
 
 def window_bytes(g, window=10, sinks=4, p=None):
@@ -291,5 +296,30 @@ def test_window_workspace():
     # the sums' end counts as the workspace's too
     assert call_window_back(g, ws=g.dk.data - need + 256) == mm.MUON_ERR_ALIAS
     assert passed(call_window_back(g, ws=g.dk.data - need))
-    assert mm.lib().muon_window_attention(None, 4, 0, ctypes.byref(packing()), None) == mm.MUON_ERR_INVALID_ARG
-    assert mm.lib().muon_window_attention(ctypes.byref(attention()), 4, 0, None, None) == mm.MUON_ERR_INVALID_ARG
+    assert mm.lib().muon_window_attention(None, 4, 0, ctypes.byref(packing()), None, 0, None) == mm.MUON_ERR_INVALID_ARG
+    assert mm.lib().muon_window_attention(ctypes.byref(attention()), 4, 0, None, None, 0, None) == mm.MUON_ERR_INVALID_ARG
+
+
+def test_window_forward_workspace():
+    """Room for the work items' largest logits, where there are many of them."""
+    a, many = attention(), packing(tokens=100, tiles=1000)
+    assert forward_bytes(a, p=many) == 4000 * 4 // 256 * 256 + 256 and mm.muon_last_error() == ""
+    assert forward_bytes(a) == 0 and mm.muon_last_error() == ""            # few items
+    assert forward_bytes(a, 100, p=many) == 0 and mm.muon_last_error() == ""   # nothing hidden
+    none = attention()
+    none.max_logit = 0
+    assert forward_bytes(none, p=many) == 0 and mm.muon_last_error() == ""
+    for window, sinks in ((0, 0), (10, -1), (10, 129)):
+        assert forward_bytes(a, window, sinks, many) == 0 and mm.muon_last_error()
+    a.heads = 5
+    assert forward_bytes(a, p=many) == 0 and mm.muon_last_error()
+    assert mm.lib().muon_window_attention_workspace_bytes(None, 1, 0, ctypes.byref(many)) == 0 and mm.muon_last_error()
+    a = attention()
+    need = forward_bytes(a, p=many)
+    assert passed(call_window(a, p=many)) and passed(call_window(a, p=many, ws=BASE * 30, ws_bytes=need))
+    assert call_window(a, p=many, ws=BASE * 30, ws_bytes=need - 1) == mm.MUON_ERR_WORKSPACE
+    assert call_window(a, p=many, ws=BASE * 30 + 64, ws_bytes=need + 64) == mm.MUON_ERR_WORKSPACE
+    for other in (a.q.data, a.v.data, a.o.data, a.lse, a.max_logit, BASE):
+        assert call_window(a, p=many, ws=other // 256 * 256, ws_bytes=need) == mm.MUON_ERR_ALIAS
+    # one that is not used overlaps nothing
+    assert passed(call_window(a, ws=a.q.data, ws_bytes=0))

@@ -183,6 +183,45 @@ def test_max_logit_is_of_visible_pairs(mm):
         assert abs(top.item() - s[ref.seen(300, 10, sinks)].max()) <= 1e-2 and top.item() >= want - 64
 
 
+def test_max_logit_of_many_items(mm):
+    """Joined in the workspace: the largest of several calls, per head and per group, NaN and infinities among them,
+    with a workspace or (through the C interface) without."""
+    print("[case] max_logit of many items", flush=True)
+    import ctypes
+
+    from matrix_muon_step_amd import binding as bd
+    lens, H, K, D, window, sinks = [700, 1, 300, 129], 60, 20, 64, 50, 2
+    q, k, v, _ = inputs(lens, H, K, D, layout="plain")
+    q[710, 7, 3] = math.nan
+    q[5, 8], k[3, 2] = 0, 1.0
+    q[5, 8, 0], k[3, 2, 0] = math.inf, 1.0               # row 5 sees key 3: +infinity
+    p = mm.muon_packing_create(lens)
+    T = sum(lens)
+    want = np.array([ref.logits(host(q, T)[r, h], host(k, T)[r, h // 3], D ** -0.5, ref.seen(n, window, sinks)).max()
+                     for h in range(H) for r, n in list(ref.spans(lens))]).reshape(H, -1)
+    want = np.where(np.isnan(want).any(axis=1), np.nan, want.max(axis=1))
+    err = 4 * 66 * 2.0 ** -24 * np.abs(np.nan_to_num(want, posinf=0.0)) + 1e-3
+    o, lse = torch.empty_like(q), torch.empty((H, T), device="cuda")
+    for entries, expect in ((H, want), (K, want.reshape(K, 3).max(axis=1))):
+        for start in (-math.inf, 5.0):
+            top = torch.full((entries,), start, device="cuda")
+            mm.muon_attention(q, k, v, p, max_logit=top, window=window, sinks=sinks, o=o, lse=lse)
+            again = torch.full((entries,), start, device="cuda")
+            args = bd.muon_attention_t(*[bd._heads_tensor("", t, T, None)[0] for t in (q, k, v, o)], lse.data_ptr(), T,
+                                       again.data_ptr(), entries, H, K, D, D ** -0.5)
+            assert mm.lib().muon_window_attention_workspace_bytes(ctypes.byref(args), window, sinks, ctypes.c_void_p(p._h)) > 0
+            assert mm.lib().muon_window_attention(ctypes.byref(args), window, sinks, ctypes.c_void_p(p._h), None, 0,
+                                                  ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == mm.MUON_OK
+            torch.cuda.synchronize()
+            assert torch.equal(top.view(torch.int32), again.view(torch.int32))
+            got, w = top.cpu().numpy().astype(np.float64), np.fmax(expect, start)
+            w = np.where(np.isnan(expect), np.nan, w)
+            assert (np.isnan(got) == np.isnan(w)).all() and (np.isposinf(got) == np.isposinf(w)).all()
+            fine = np.isfinite(w)
+            e = err.reshape(entries, -1).max(axis=1)
+            assert (np.abs(got[fine] - w[fine]) <= e[fine]).all()
+
+
 def test_streams_and_graphs(mm):
     """Captured forward and backward calls of two layers that share a workspace, replayed with eager work between."""
     print("[case] captured", flush=True)
