@@ -451,7 +451,9 @@ muon_status_t muon_attention_backward(const muon_attention_grad_t* args, muon_pa
  * args' pointers only max_logit being NULL is looked at) max_logit is raised
  * with fewer atomics.  The backward workspace holds,
  * beside muon_attention_backward's, 8 * head_dim * kv_heads * sinks bytes for
- * every 256 rows (or fewer) of a sequence, where the window hides any. */
+ * every 256 rows (or fewer) of a sequence, where the window hides any, and up to
+ * 1024 * head_dim * heads for every 128 (or fewer) where that makes few key
+ * heads or rows faster. */
 #define MUON_MAX_SINKS 128
 size_t muon_window_attention_workspace_bytes(const muon_attention_t* args, int64_t window, int64_t sinks,
                                              muon_packing_t packing);

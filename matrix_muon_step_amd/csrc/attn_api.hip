@@ -116,11 +116,41 @@ size_t row_bytes(int32_t heads, muon_packing_t p) {
   return align_up(static_cast<size_t>(row_stride(p)) * heads * 2 * sizeof(float));
 }
 
+size_t far_bytes(const muon_attention_grad_t& g, const Window* w, muon_packing_t p) {
+  if (!has_far(w, p)) return 0;
+  return align_up(static_cast<size_t>(p->chunks) * g.kv_heads * 2 * static_cast<size_t>(w->sinks) * g.head_dim * sizeof(float));
+}
+
+size_t part_bytes(const muon_attention_grad_t& g, muon_packing_t p, int32_t parts) {
+  return parts == 1 ? 0 : static_cast<size_t>(p->n_tiles) * g.kv_heads * parts * 2 * kAttnRows * g.head_dim * sizeof(float);
+}
+
+// Work-groups that share a key tile's query heads in dK/dV, where key tiles
+// are few.  One holds a compute unit (of 256) for about 6 us and, for each tile
+// of rows and head, 2.4 us (heads of up to 64: 1.3); shares cost a launch and
+// their float32 sums, written and read again.  Backward pass in us, one
+// work-group | this many: 8/1 heads of 128, 4096 tokens, window 1024 265 | 88
+// (8); 8192, window 4096 1027 | 464 (4); 16/4 of 128, 4096, window 1024 180 | 139
+// (2), window 256 119 | 112 (2); 32/8 of 128, 2048, window 64 107 | 90 (2); 8192
+// tokens of 32/4 (256 key tiles), window 256 270 | 297 (2).
+int32_t key_parts(const muon_attention_grad_t& g, const Window* w, muon_packing_t p) {
+  if (!hides(w, p)) return 1;
+  const int32_t group = g.heads / g.kv_heads;
+  const int64_t items = p->n_tiles * g.kv_heads;
+  const double turns = static_cast<double>((std::min<int64_t>(p->longest, kAttnRows - 1 + w->window) + kAttnStep - 1) / kAttnStep);
+  auto time = [&](int32_t parts) {
+    const double rounds = static_cast<double>((items * parts + 255) / 256);
+    const double turn = g.head_dim > 64 ? 2.4 : 1.3, share = (group + parts - 1) / parts;
+    return rounds * (6.0 + turns * share * turn) + (parts > 1 ? 4.0 + 2e-6 * static_cast<double>(part_bytes(g, p, parts)) / 12 : 0.0);
+  };
+  int32_t best = 1;
+  for (int32_t parts = 2; parts <= std::min(group, 8); ++parts)
+    if (time(parts) < 0.9 * time(best)) best = parts;
+  return best;
+}
+
 size_t backward_bytes(const muon_attention_grad_t& g, const Window* w, muon_packing_t p) {
-  size_t bytes = row_bytes(g.heads, p);
-  if (has_far(w, p))
-    bytes += align_up(static_cast<size_t>(p->chunks) * g.kv_heads * 2 * static_cast<size_t>(w->sinks) * g.head_dim *
-                      sizeof(float));
+  size_t bytes = row_bytes(g.heads, p) + far_bytes(g, w, p) + part_bytes(g, p, key_parts(g, w, p));
   return bytes;
 }
 
@@ -320,6 +350,10 @@ muon_status_t attention_backward(const muon_attention_grad_t* args, const Window
     a.far = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + row_bytes(g.heads, packing));
     a.far_joined = (packing->longest + kFarRows - 1) / kFarRows - w->window / kFarRows > kFarDirect;
   }
+  a.key_parts = key_parts(g, w, packing);
+  if (a.key_parts > 1)
+    a.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + row_bytes(g.heads, packing) +
+                                       far_bytes(g, w, packing));
   const hipError_t e =
       (windowed ? launch_window_attention_backward : launch_attention_backward)(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MUON_OK : hip_fail(e, "attention backward launch");

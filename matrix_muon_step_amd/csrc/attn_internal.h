@@ -64,6 +64,8 @@ struct AttnArgs {
   int32_t window, sinks;       // row i sees key j <= i where i - j < window or j < sinks
   float* far;                  // backward workspace: sums over rows beyond their windows (NULL: there are none)
   int32_t far_joined;          // the first chunk's sums are a sequence's
+  int32_t key_parts;           // backward: work-groups that share a key tile's query heads
+  float* parts;                // backward workspace: their sums, where there are several
   float* tops;                 // forward workspace: heads x n_tiles, each item's largest logit, or NULL
 };
 

@@ -681,6 +681,12 @@ __device__ __forceinline__ float* far_sum(const AttnArgs& a, int slot, int kv) {
   return a.far + (static_cast<int64_t>(slot) * a.kv_heads + kv) * (2 * a.sinks * a.head_dim);
 }
 
+// Where a share of a key tile's sums lies: dK (which = 0) or dV (1), kAttnRows x head_dim.
+__device__ __forceinline__ float* part_sum(const AttnArgs& a, int tile, int kv, int part, int which) {
+  const int64_t i = ((static_cast<int64_t>(tile) * a.kv_heads + kv) * a.key_parts + part) * 2 + which;
+  return a.parts + i * (kAttnRows * a.head_dim);
+}
+
 // Four consecutive per-row values of a tile.
 __device__ __forceinline__ f32x4_t row_values(const LAS unsigned char* __restrict__ p) { return *(const LAS f32x4_t*)p; }
 
@@ -783,16 +789,15 @@ struct QueryStream {
     const int range = (kAttnRows - 1 + a.window + kAttnStep - 1) / kAttnStep;
     return min(range - 1 - t.first / kAttnStep % range, nq - 1);
   }
-  __device__ __forceinline__ QueryStream(const AttnArgs& a, const AttnTile& t, int kv, int nq, int wave, int lane)
-      : ql(a.q, t.row0 + static_cast<int64_t>(t.first) + start(a, t, nq) * kAttnStep, kv * (a.heads / a.kv_heads), a.head_dim,
-           wave, lane),
-        gl(a.d_o, t.row0 + static_cast<int64_t>(t.first) + start(a, t, nq) * kAttnStep, kv * (a.heads / a.kv_heads),
-           a.head_dim, wave, lane) {
-    group = a.heads / a.kv_heads;
+  // `count` query heads from head0 on.
+  __device__ __forceinline__ QueryStream(const AttnArgs& a, const AttnTile& t, int head0, int count, int nq, int wave, int lane)
+      : ql(a.q, t.row0 + static_cast<int64_t>(t.first) + start(a, t, nq) * kAttnStep, head0, a.head_dim, wave, lane),
+        gl(a.d_o, t.row0 + static_cast<int64_t>(t.first) + start(a, t, nq) * kAttnStep, head0, a.head_dim, wave, lane) {
+    group = count;
     row = t.first + start(a, t, nq) * kAttnStep;
     if (WIN) wrap = nq * kAttnStep;
     head = fill = 0;
-    stat = (wave == 0 ? a.row_lse2 : a.row_delta) + kv * group * a.row_stride + t.row0 + row;
+    stat = (wave == 0 ? a.row_lse2 : a.row_delta) + head0 * a.row_stride + t.row0 + row;
     stat_stride = a.row_stride;
     q_head = a.q.hs * 2;
     g_head = a.d_o.hs * 2;
@@ -860,9 +865,16 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
   LAS unsigned char* lds = (LAS unsigned char*)smem;
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kv = blockIdx.x % a.kv_heads;
-  const AttnTile t = a.by_key[blockIdx.x / a.kv_heads];
-  const int group = a.heads / a.kv_heads;
+  // With a window a key tile's query heads may be shared out over several work-groups.
+  const int items = WIN ? a.kv_heads * a.key_parts : a.kv_heads, item = blockIdx.x % items;
+  const int kv = WIN ? item % a.kv_heads : item, part = WIN ? item / a.kv_heads : 0;
+  const AttnTile t = a.by_key[blockIdx.x / items];
+  int head0 = kv * (a.heads / a.kv_heads), group = a.heads / a.kv_heads;
+  if (WIN) {
+    const int from = part * group / a.key_parts, to = (part + 1) * group / a.key_parts;
+    head0 += from;
+    group = to - from;
+  }
   const int nq = query_tiles<WIN>(a, t);
   const int total = nq * group;
   const int wk0 = t.first + 32 * (wave & 3), half = wave >> 2;
@@ -870,7 +882,7 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
   const float c = a.scale * kAttnLog2e;
 
   const FragOff fo = frag_offsets(lane);
-  QueryStream<DP, EXACT, 8, WIN> stream(a, t, kv, nq, wave, lane);
+  QueryStream<DP, EXACT, 8, WIN> stream(a, t, head0, group, nq, wave, lane);
   const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
   bf16x8_t kf[G::KS], vf[G::KS];
   own_rows<DP>(a.k.p + (krow0 * a.k.ts + kv * a.k.hs) * 2, a.k.ts, a.head_dim, t.len - wk0, lane, kf);
@@ -933,6 +945,19 @@ __global__ __launch_bounds__(512, 2) void attention_dkv_pair_kernel(const AttnAr
     dkv_sums<DP>(lds + cur + sum_of, fo, half, own, acc);
     dkv_sums<DP>(lds + cur + sum_of, fo, half ^ 1, other, acc);
   }
+  if (WIN && a.key_parts > 1) {
+    if (key >= t.len) return;
+    float* p = part_sum(a, blockIdx.x / items, kv, part, half == 0 ? 1 : 0) + (key - t.first) * a.head_dim;
+#pragma unroll
+    for (int db = 0; db < G::DB; ++db)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int d = 32 * db + 8 * g + 4 * h;
+        const f32x16_t& x = acc[db];
+        if (d < a.head_dim) gst(p + d, (f32x4_t){x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]});
+      }
+    return;
+  }
   if (WIN) add_far<DP>(a, t, kv, key, half == 0 ? 1 : 0, h, acc);
   const int64_t row = static_cast<int64_t>(t.row0) + key;
   store_rows<DP>(half == 0 ? a.dv : a.dk, row, kv, a.head_dim, key < t.len, lane, acc, half == 0 ? 1.f : a.scale);
@@ -959,7 +984,7 @@ __global__ __launch_bounds__(256, 3) void attention_dkv_kernel(const AttnArgs a)
   const int key = wk0 + (lane & 31);
   const float c = a.scale * kAttnLog2e;
   const FragOff fo = frag_offsets(lane);
-  QueryStream<DP, EXACT, 4, WIN> stream(a, t, kv, nq, wave, lane);
+  QueryStream<DP, EXACT, 4, WIN> stream(a, t, kv * (a.heads / a.kv_heads), a.heads / a.kv_heads, nq, wave, lane);
   int q0 = stream.row, head = 0, cur = 0;
   stream.template next<2>(t.len, t.first, lds, wave);
   const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
@@ -1049,6 +1074,8 @@ hipError_t forward(const AttnArgs& a, hipStream_t s) {
 // The sums that rows beyond their windows give the first tokens (windowed calls only).
 template <int DP, bool EXACT>
 hipError_t far_rows(const AttnArgs& a, hipStream_t s);
+// The sums of key tiles whose query heads were shared out.
+hipError_t join_parts(const AttnArgs& a, hipStream_t s);
 
 template <int DP, bool EXACT, bool WIN>
 hipError_t backward(const AttnArgs& a, hipStream_t s) {
@@ -1060,7 +1087,7 @@ hipError_t backward(const AttnArgs& a, hipStream_t s) {
     if (e == hipSuccess) e = far_rows<DP, EXACT>(a, s);
   }
   if (e != hipSuccess) return e;
-  const dim3 grid(static_cast<uint32_t>(a.n_tiles) * a.kv_heads);
+  const dim3 grid(static_cast<uint32_t>(a.n_tiles) * a.kv_heads * (WIN ? a.key_parts : 1));
   // Up to two key tiles for each of the 256 compute units, the longest one's
   // turns are what takes the time, and the pair kernel's are half as long;
   // with more the three-to-a-unit kernel wins.  dQ, dK and dV with heads of 64,
@@ -1071,8 +1098,12 @@ hipError_t backward(const AttnArgs& a, hipStream_t s) {
   // wins from fewer on: window 512, 1290 tokens, 25 heads (275) 51.7 | 58.8; 4096,
   // 12 heads (384) 75 | 67; window 1024, 2500, 25 heads (500) 94 | 82; window
   // 2048, 4096, 12 heads 120 | 134.
-  if (DP == 64 && grid.x > (WIN && a.longest <= 1280 ? 320 : 512)) hipLaunchKernelGGL((attention_dkv_kernel<64, EXACT, WIN>), grid, dim3(256), 0, s, a);
+  if (DP == 64 && (!WIN || a.key_parts == 1) && grid.x > (WIN && a.longest <= 1280 ? 320 : 512)) hipLaunchKernelGGL((attention_dkv_kernel<64, EXACT, WIN>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((attention_dkv_pair_kernel<DP, EXACT, WIN>), grid, dim3(512), 0, s, a);
+  if constexpr (WIN) {
+    e = hipGetLastError();
+    return e == hipSuccess ? join_parts(a, s) : e;
+  }
   return hipGetLastError();
 }
 

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256, 2) void attention_far_kernel(const AttnArgs a)
   const int key = wk0 + (lane & 31);
   const float c = a.scale * kAttnLog2e;
   const FragOff fo = frag_offsets(lane);
-  QueryStream<DP, EXACT, 4, false> stream(a, rows, kv, nq, wave, lane);
+  QueryStream<DP, EXACT, 4, false> stream(a, rows, kv * (a.heads / a.kv_heads), a.heads / a.kv_heads, nq, wave, lane);
   int q0 = stream.row, head = 0, cur = 0;
   stream.template next<2>(t.len, 0, lds, wave);
   const int64_t krow0 = static_cast<int64_t>(t.row0) + wk0;
@@ -126,6 +126,39 @@ __global__ __launch_bounds__(256) void attention_far_join_kernel(const AttnArgs 
   __syncthreads();
   if (wave > 0 || !there) return;
   gst(p, ((sum + part[64 + lane]) + part[128 + lane]) + part[192 + lane]);
+}
+
+// dK (blockIdx.y even) or dV of 32 keys of a tile from the shares of its query
+// heads, in order, and then the sums over rows beyond their windows.
+__global__ __launch_bounds__(256) void attention_part_join_kernel(const AttnArgs a) {
+  const int tile = blockIdx.x / a.kv_heads, kv = blockIdx.x % a.kv_heads;
+  const AttnTile t = a.by_key[tile];
+  const int which = blockIdx.y & 1, row0 = 32 * (blockIdx.y >> 1), per_key = a.head_dim / 4;
+  const HeadsView& v = which ? a.dv : a.dk;
+  const float mul = which ? 1.f : a.scale;
+  const int64_t step = part_sum(a, 0, 0, 1, 0) - part_sum(a, 0, 0, 0, 0);
+  const int first = a.window / kFarRows, end = a.far_joined ? first + 1 : (t.len + kFarRows - 1) / kFarRows;
+  for (int i = threadIdx.x; i < 32 * per_key; i += 256) {
+    const int row = row0 + i / per_key, d = i % per_key * 4, key = t.first + row;
+    if (key >= t.len) continue;
+    const float* p = part_sum(a, tile, kv, 0, which) + row * a.head_dim + d;
+    f32x4_t sum = gld<f32x4_t>(p);
+    for (int j = 1; j < a.key_parts; ++j) sum += gld<f32x4_t>(p + j * step);
+    if (a.far && key < a.sinks && t.len > a.window)
+      for (int c = first; c < end; ++c)
+        sum += gld<f32x4_t>(far_sum(a, t.chunk + c, kv) + (which * a.sinks + key) * a.head_dim + d);
+    uint2 u;
+    u.x = pack_bf16(sum[0] * mul, sum[1] * mul);
+    u.y = pack_bf16(sum[2] * mul, sum[3] * mul);
+    gst(v.p + ((static_cast<int64_t>(t.row0) + key) * v.ts + kv * v.hs + d) * 2, u);
+  }
+}
+
+hipError_t join_parts(const AttnArgs& a, hipStream_t s) {
+  if (a.key_parts == 1) return hipSuccess;
+  hipLaunchKernelGGL(attention_part_join_kernel, dim3(static_cast<uint32_t>(a.n_tiles) * a.kv_heads, 2 * kAttnRows / 32),
+                     dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 // An entry's largest logit over the items of its heads, which lie together.

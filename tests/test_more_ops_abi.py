@@ -323,3 +323,17 @@ def test_window_forward_workspace():
         assert call_window(a, p=many, ws=other // 256 * 256, ws_bytes=need) == mm.MUON_ERR_ALIAS
     # one that is not used overlaps nothing
     assert passed(call_window(a, ws=a.q.data, ws_bytes=0))
+
+
+def test_window_workspace_of_few_key_heads():
+    """Room for float32 sums where several work-groups share a key tile, within what the header says."""
+    def extra(heads, kv, dim, tiles, tokens, window=1000):
+        g, p = attention_grad(heads, kv, dim), packing(tokens, tiles)
+        return window_bytes(g, window, 0, p) - mm.lib().muon_attention_backward_workspace_bytes(ctypes.byref(g), ctypes.byref(p))
+
+    for heads, kv, dim, tiles in ((8, 1, 128, 32), (32, 8, 128, 16), (16, 2, 40, 10), (24, 3, 64, 32)):
+        more = extra(heads, kv, dim, tiles, 128 * tiles)
+        assert 0 < more <= tiles * 1024 * dim * heads
+    assert extra(8, 8, 128, 32, 4096) == 0                 # no heads to share out
+    assert extra(32, 8, 128, 200, 25600) == 0              # enough key tiles
+    assert extra(8, 1, 128, 32, 4096, window=4096) == 0    # nothing hidden
