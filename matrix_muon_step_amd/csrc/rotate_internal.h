@@ -6,13 +6,22 @@
 
 namespace muon {
 
-// Tokens of one work item, a piece of a packing's 128-row tile.
+// Tokens of one work item, a piece of a packing's 128-row tile: few enough for
+// many work items, enough to pay for a token's angles.  16384 tokens, 32/8
+// heads of 128, us, forward / gradient: 8 68 / 109, 16 72 / 114; 4100 tokens, 25/25
+// heads of 64 14.3 / 26.8 and 13.8 / 24.2 (2 and 4 were slower in a first form).
 constexpr int kRotateRows = 8;
 constexpr int kRotatePieces = kAttnRows / kRotateRows;
 // Work-groups of the backward kernel at most, for each of the two tensors, each
-// with one partial sum of the weights' gradients in the workspace.
+// with one partial sum of the weight's gradient in the workspace (the 16384
+// tokens: 512 103 us, 1024 109, 2048 112).
 constexpr int kRotateGroups = 512;
 constexpr int kRotateLanes = 256;
+// A call whose tensors are more bytes than the memory-side cache holds writes
+// past the caches.  Forward in us, through | past them, with the inputs in the
+// cache and not: 16384 tokens, 32/8 heads of 128 (336 MB) 68 | 52 and 67 | 66; 25/25
+// heads of 64 (210 MB) 33 | 40 and 42.5 | 45.6.  (Reads past them too were slower
+// wherever the cache held the inputs.)
 constexpr int64_t kRotateLarge = int64_t{256} << 20;
 
 // One of the two tensors of a call.

@@ -266,7 +266,9 @@ struct Part {
 // ------------------------------------------------------------------ forward
 // Queries and keys in work-groups of their own (blockIdx.y), here and in the
 // backward pass: twice as many for short calls, one weight (and its gradient)
-// in registers at a time.
+// in registers at a time.  Bound by memory: 16384 tokens, 32/8 heads of 128, three
+// axes 66 us (5.1 TB/s) from memory, 52 where the inputs are in the cache; a
+// short call is one round of start, load, store: 8 tokens 5 us.
 template <int P, bool INTER, bool NORM, bool STREAM>
 __global__ __launch_bounds__(kRotateLanes) void rotate_kernel(const RotateArgs a) {
   __shared__ __align__(16) Angles angles;
@@ -308,7 +310,10 @@ __global__ __launch_bounds__(kRotateLanes) void rotate_kernel(const RotateArgs a
 }
 
 // ----------------------------------------------------------------- backward
-// Without a norm the gradient is dz turned back.
+// Without a norm the gradient is dz turned back.  The same tokens 100 us (5.0
+// TB/s), half of it also in the vector unit: about 250 instructions for a
+// lane's 16 elements.  The next head's loads are under way while one is worked
+// on (without that 118 us), in 128 registers for four waves to a SIMD.
 template <int P, bool INTER, bool NORM, bool STREAM>
 __global__ __launch_bounds__(kRotateLanes, 4) void rotate_backward_kernel(const RotateArgs a) {
   __shared__ __align__(16) Angles angles;
