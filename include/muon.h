@@ -325,7 +325,9 @@ muon_status_t muon_qk_clip(const muon_qk_clip_matrix_t* mats, int64_t n, float t
  * logit (QK-Clip's input); a saved 8-bit activation and the upstream
  * gradient give a projection's G.  They were added within
  * MUON_ABI_VERSION 7, since no earlier entry point changed: a caller that
- * loads the library at run time looks for muon_packing_create by name.
+ * loads the library at run time looks for muon_packing_create by name (and, for
+ * windowed attention, norms and rotations and clipping, which came after the
+ * rest, for muon_grad_norm).
  *
  * As for the step calls: host structures are read only during the call,
  * device memory is the caller's, everything is validated before anything is

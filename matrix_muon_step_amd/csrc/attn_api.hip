@@ -137,11 +137,13 @@ int32_t key_parts(const muon_attention_grad_t& g, const Window* w, muon_packing_
   if (!hides(w, p)) return 1;
   const int32_t group = g.heads / g.kv_heads;
   const int64_t items = p->n_tiles * g.kv_heads;
-  const double turns = static_cast<double>((std::min<int64_t>(p->longest, kAttnRows - 1 + w->window) + kAttnStep - 1) / kAttnStep);
+  const double turns =
+      static_cast<double>((std::min<int64_t>(p->longest, kAttnRows - 1 + w->window) + kAttnStep - 1) / kAttnStep);
   auto time = [&](int32_t parts) {
     const double rounds = static_cast<double>((items * parts + 255) / 256);
     const double turn = g.head_dim > 64 ? 2.4 : 1.3, share = (group + parts - 1) / parts;
-    return rounds * (6.0 + turns * share * turn) + (parts > 1 ? 4.0 + 2e-6 * static_cast<double>(part_bytes(g, p, parts)) / 12 : 0.0);
+    const double join = parts > 1 ? 4.0 + 2e-6 * static_cast<double>(part_bytes(g, p, parts)) / 12 : 0.0;
+    return rounds * (6.0 + turns * share * turn) + join;
   };
   int32_t best = 1;
   for (int32_t parts = 2; parts <= std::min(group, 8); ++parts)
@@ -150,8 +152,7 @@ int32_t key_parts(const muon_attention_grad_t& g, const Window* w, muon_packing_
 }
 
 size_t backward_bytes(const muon_attention_grad_t& g, const Window* w, muon_packing_t p) {
-  size_t bytes = row_bytes(g.heads, p) + far_bytes(g, w, p) + part_bytes(g, p, key_parts(g, w, p));
-  return bytes;
+  return row_bytes(g.heads, p) + far_bytes(g, w, p) + part_bytes(g, p, key_parts(g, w, p));
 }
 
 }  // namespace
