@@ -484,9 +484,10 @@ muon_status_t muon_window_attention_backward(const muon_attention_grad_t* args, 
  *   rotary.frequency    HOST, rotary_dim / 2 radians per position, each of
  *                       magnitude <= MUON_MAX_FREQUENCY
  *   rotary.axis         HOST, each pair's axis (0 .. axes - 1), or NULL: 0
- *   positions  DEVICE, axes rows of position_stride (>= the packing's tokens)
- *              integers of position_bits (32 or 64), of any sign and size; or
- *              NULL: each token's index in its sequence, on every axis
+ *   positions  DEVICE, axes rows of position_stride (>= the packing's tokens, or
+ *              0: one row for every axis) integers of position_bits (32 or 64),
+ *              of any sign and size; or NULL: each token's index in its
+ *              sequence, on every axis
  *   weights    DEVICE, head_dim float32, or NULL: ones (and so without a norm)
  *   eps        finite, >= 2^-126 (norm only)
  *   heads, kv_heads  1 .. MUON_MAX_HEADS each; head_dim as for attention

@@ -1129,9 +1129,9 @@ def muon_qk_norm_rotate(q, k, packing: MuonPacking, rotary: Optional[MuonRotary]
     token's position, unless `rotary` is None.  Returns (q_out, k_out).
 
     q is (rows, heads, head_dim), k (rows, kv_heads, head_dim), bfloat16, views
-    taken as they are.  positions: int32 or int64, (tokens) or (axes, tokens);
-    default: each token's index in its sequence, on every axis.  q_out may be q
-    and k_out k.  Outputs given by the caller keep what they hold in rows behind
+    taken as they are.  positions: int32 or int64, (tokens) or (axes, tokens),
+    one row expanded over the axes too; default: each token's index in its
+    sequence, on every axis.  q_out may be q and k_out k.  Outputs given by the caller keep what they hold in rows behind
     the last sequence; outputs made here are views of one buffer and hold zeros
     there.  stream: as for muon_attention."""
     rows = q.shape[0]

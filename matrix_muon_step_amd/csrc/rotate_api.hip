@@ -90,8 +90,8 @@ muon_status_t check(const Call& c, muon_packing_t packing, const std::vector<Ran
   if (a.positions && tokens > 0 && a.rotary.rotary_dim > 0) {
     if (a.position_bits != 32 && a.position_bits != 64)
       return fail(MUON_ERR_INVALID_ARG, "muon: position_bits must be 32 or 64");
-    if (a.position_stride < tokens || a.position_stride > (int64_t{1} << 40))
-      return fail(MUON_ERR_INVALID_ARG, "muon: position_stride must be the packing's tokens to 2^40");
+    if (a.position_stride != 0 && (a.position_stride < tokens || a.position_stride > (int64_t{1} << 40)))
+      return fail(MUON_ERR_INVALID_ARG, "muon: position_stride must be 0 or the packing's tokens to 2^40");
     const int width = a.position_bits / 8;
     st = add(a.positions, ((a.rotary.axes - 1) * a.position_stride + tokens) * width, width, false, "positions");
     if (st != MUON_OK) return st;

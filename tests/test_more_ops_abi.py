@@ -154,6 +154,9 @@ def test_rotate_passes_on():
         assert passed(call(a))
         a = rotate(kv=3)                                # queries and keys need not be grouped
         assert passed(call(a))
+        a = rotate(rotary=mm.MuonRotary(64, sections=[8, 12, 12]))
+        a.position_stride = 0                           # one row of positions for all axes
+        assert passed(call(a))
     a = rotate()
     assert passed(call_rotate_back(a, up_q=a.q_out, up_k=a.k_out))
     a.norm, a.q_weight, a.k_weight, a.q.data, a.k.data = 0, 0, 0, 0, 0

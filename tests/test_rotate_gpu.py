@@ -137,6 +137,7 @@ def test_positions(mm, axes, dtype):
     check(mm, [90], 2, 2, 40, mm.MuonRotary(40, pair_axes=pair_axes, interleaved=True), positions=p, behind=5)
     if axes == 1:
         check(mm, [90], 2, 2, 40, mm.MuonRotary(40), positions=p[0], behind=5)
+    check(mm, [40, 50], 4, 2, 64, mm.MuonRotary(64, sections=sections), positions=p[:1].expand(axes, rows), behind=5)
 
 
 def test_frequencies(mm):
