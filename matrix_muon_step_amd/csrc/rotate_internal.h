@@ -17,6 +17,9 @@ constexpr int kRotatePieces = kAttnRows / kRotateRows;
 // tokens: 512 103 us, 1024 109, 2048 112).
 constexpr int kRotateGroups = 512;
 constexpr int kRotateLanes = 256;
+// Heads of a lane's float32 sums of the weight's gradient at most: with the
+// rounding of a work-group's partial sum below 64 half steps of what is added.
+constexpr int kRotateRun = 60;
 // A call whose tensors are more bytes than the memory-side cache holds writes
 // past the caches.  Forward in us, through | past them, with the inputs in the
 // cache and not: 16384 tokens, 32/8 heads of 128 (336 MB) 68 | 52 and 67 | 66; 25/25

@@ -124,6 +124,22 @@ struct Place {
       hi = lo + (D - R) / 2;
     }
   }
+  // Which lane of a head holds element d, and at which of its 2 P places.
+  static __device__ __forceinline__ void of_element(const RotateArgs& a, int d, int& lane, int& k) {
+    if (INTER) {
+      lane = d / (2 * P);
+      k = d % (2 * P);
+      return;
+    }
+    const int R = a.rotary_dim;
+    const bool rest = d >= R;
+    const int half = (rest ? a.head_dim - R : R) / 2;
+    if (rest) d -= R;
+    const bool high = d >= half;
+    if (high) d -= half;
+    lane = (rest ? R / (2 * P) : 0) + d / P;
+    k = (high ? P : 0) + d % P;
+  }
   // x turned by the angles (BACK: against them), in place.
   template <bool BACK>
   __device__ __forceinline__ void turn(const Angles& angles, int first, float (&x)[2 * P]) const {
@@ -314,6 +330,10 @@ __global__ __launch_bounds__(kRotateLanes) void rotate_kernel(const RotateArgs a
 // TB/s), half of it also in the vector unit: about 250 instructions for a
 // lane's 16 elements.  The next head's loads are under way while one is worked
 // on (without that 118 us), in 128 registers for four waves to a SIMD.
+//
+// A lane adds a weight's gradient up in float32 over runs of at most
+// kRotateRun heads, and the runs in float64 in LDS (each lane for itself), so
+// that the error does not grow with the tokens.
 template <int P, bool INTER, bool NORM, bool STREAM>
 __global__ __launch_bounds__(kRotateLanes, 4) void rotate_backward_kernel(const RotateArgs a) {
   __shared__ __align__(16) Angles angles;
@@ -323,10 +343,22 @@ __global__ __launch_bounds__(kRotateLanes, 4) void rotate_backward_kernel(const 
   const int half = a.rotary_dim >> 1, lo = 2 * place.lo, hi = 2 * place.hi, D = a.head_dim;
   const float share = 1.f / static_cast<float>(D);
   const int64_t pieces = int64_t{a.n_tiles} * kRotatePieces;
+  // The lanes' sums of ended runs: all lanes' first places, then the second, ...
+  constexpr int LINE = kRotateLanes + 1;
+  __shared__ double part[LINE * 2 * P], sums[kRotateLanes];
   float w[2 * P], dw[2 * P];
   if (NORM) load_weight<P>(t.weight, place.lo, place.hi, w);
 #pragma unroll
   for (int k = 0; k < 2 * P; ++k) dw[k] = 0.f;
+  bool ended = false;
+  auto end_run = [&]() {
+#pragma unroll
+    for (int k = 0; k < 2 * P; ++k) {
+      part[k * LINE + threadIdx.x] += dw[k];
+      dw[k] = 0.f;
+    }
+  };
+  int run = 0;  // heads of the run so far, at most
   for (int64_t i = blockIdx.x; i < pieces; i += gridDim.x) {
     const Piece piece(a, i);
     if (piece.n <= 0) continue;
@@ -334,10 +366,26 @@ __global__ __launch_bounds__(kRotateLanes, 4) void rotate_backward_kernel(const 
     Part<P> up, up_next, x, x_next;
     up.load(walk.p[0], lo, hi);
     if (NORM) x.load(walk.p[2], lo, hi);
+    if (NORM) {
+      const int most = (piece.n * t.heads + slots - 1) / slots;  // heads of the piece to a lane
+      if (run + most > kRotateRun) {
+        if (!ended) {
+          for (int k = 0; k < 2 * P; ++k) part[k * LINE + threadIdx.x] = 0.0;
+        }
+        ended = true;
+        end_run();
+        run = 0;
+      }
+      run = min(run + most, kRotateRun);
+    }
     __syncthreads();
     fill_angles(a, piece.row, piece.index, piece.n, angles);
     __syncthreads();
-    while (walk.left > 0) {
+    for (int of_run = 0; walk.left > 0; ++of_run) {
+      if (NORM && of_run == kRotateRun) {
+        end_run();
+        of_run = 0;
+      }
       unsigned char* out = walk.p[1];
       const int token = walk.token;
       walk.next();
@@ -372,24 +420,24 @@ __global__ __launch_bounds__(kRotateLanes, 4) void rotate_backward_kernel(const 
   if (!NORM || !t.d_weight) return;
   // This work-group's sums over its lanes, in a fixed order: an element's from
   // every slot, by as many lanes as there are for it.
-  __shared__ float part[kRotateLanes * 2 * P], sums[kRotateLanes];
-  if (place.live) {
 #pragma unroll
-    for (int k = 0; k < 2 * P; ++k) part[slot * D + (k < P ? place.lo + k : place.hi + k - P)] = dw[k];
-  }
+  for (int k = 0; k < 2 * P; ++k) part[k * LINE + threadIdx.x] = (ended ? part[k * LINE + threadIdx.x] : 0.0) + dw[k];
   __syncthreads();
   const int shares = kRotateLanes / D, mine = threadIdx.x / D, d = threadIdx.x - mine * D;
   if (mine < shares) {
-    float x = 0.f;
+    int lane, k;
+    Place<P, INTER>::of_element(a, d, lane, k);
+    const double* p = part + k * LINE + lane;
+    double x = 0.0;
 #pragma unroll 8
-    for (int v = mine; v < slots; v += shares) x += part[v * D + d];
+    for (int v = mine; v < slots; v += shares) x += p[v << a.group_log2];
     sums[threadIdx.x] = x;
   }
   __syncthreads();
   if (threadIdx.x < D) {
-    float x = sums[d];
+    double x = sums[d];
     for (int v = 1; v < shares; ++v) x += sums[v * D + d];
-    gst(a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + blockIdx.y) * D + d, x);
+    gst(a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + blockIdx.y) * D + d, static_cast<float>(x));
   }
 }
 
