@@ -299,6 +299,12 @@ muon_status_t muon_profile_read(double* ms, int64_t* launches);
  * by tau / max_logit[h], so its max logit becomes tau; heads at or below
  * tau (or with a NaN max logit) are not touched.  An infinite max logit
  * zeroes the head's rows.
+ *   That holds where logits are linear in both projections (rotary positions
+ * keep them so).  Behind a norm of queries and keys (muon_qk_norm_rotate with
+ * norm != 0) they do not depend on the projections' size, and clipping W_q and
+ * W_k would shrink them at every step for nothing: there the norm's weights
+ * take their place, each as one head (rows = head_dim, cols = 1), with the
+ * largest max logit of the heads that share them.
  *   W          DEVICE, rows x cols float32 row-major, 16-byte aligned,
  *              updated in place; disjoint from every other W of the call
  *   rows, cols >= 1, <= MUON_MAX_DIM; rows a multiple of head_dim
@@ -492,7 +498,8 @@ muon_status_t muon_window_attention_backward(const muon_attention_grad_t* args, 
  *   eps        finite, >= 2^-126 (norm only)
  *   heads, kv_heads  1 .. MUON_MAX_HEADS each; head_dim as for attention
  * q_out may be q itself and k_out k (the same data and strides).  Rows behind
- * the packing's last sequence are neither read nor written. */
+ * the packing's last sequence are neither read nor written.  For QK-Clip of a
+ * layer with these norms see muon_qk_clip. */
 #define MUON_MAX_AXES 4
 #define MUON_MAX_FREQUENCY 1024
 typedef struct muon_rotary {

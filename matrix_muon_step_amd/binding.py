@@ -747,7 +747,11 @@ def muon_qk_clip(matrices, tau: float, stream=None) -> None:
     """QK-Clip after a step: for each (W, head_dim, max_logit) with W a float32
     (heads * head_dim, cols) projection and max_logit a float32 tensor of
     its heads' max logits, the rows of every head with max_logit > tau are
-    scaled by sqrt(tau / max_logit) in place."""
+    scaled by sqrt(tau / max_logit) in place.
+
+    Behind a norm of queries and keys (muon_qk_norm_rotate) logits do not depend
+    on the projections' size: clip the norms' weights, (weight[:, None],
+    head_dim, max_logit.max().view(1)), instead of W_q and W_k."""
     import torch
 
     n = len(matrices)
