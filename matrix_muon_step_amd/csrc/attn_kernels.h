@@ -418,7 +418,8 @@ __device__ __forceinline__ void join_acc(const LAS unsigned char* __restrict__ p
 // each among the others', end last.  With max_logit from -infinity 33 us (see
 // atomic_max_float).
 // With a window of 1024 and 4 first tokens: 16384 tokens, 32 heads of 128 over 8,
-// 330 us, the matrix cores 44% busy (19 tiles visited for 16 that are seen, and an
+// 350 us (traced, once the card's clocks have settled; 8192^3 products ran at 1.19
+// PFLOP/s on it), the matrix cores 44% busy (19 tiles visited for 16 that are seen, and an
 // item's start and end come every 19 turns); the 4100 tokens, window 256, 22 us.
 template <int DP, bool EXACT, int SPLIT, bool WIN>
 __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kernel(const AttnArgs a) {
@@ -565,7 +566,7 @@ __global__ __launch_bounds__(256 * SPLIT, DP == 64 ? 4 : 2) void attention_kerne
 // passed on: dQ summed by atomics from the dK/dV kernel would save 2 of the 7
 // products of the two kernels, but with an order that changes from run to
 // run.  8192 tokens, 32 heads of 128: 680 us, 1.21 PFLOP/s, matrix cores 65%
-// busy (with one wave a SIMD, 1240 us).  With the window above 432 us, 49% busy.
+// busy (with one wave a SIMD, 1240 us).  With the window above 451 us, 49% busy.
 template <int DP, bool EXACT, int SPLIT, bool WIN>
 __global__ __launch_bounds__(256 * SPLIT, DP == 64 && SPLIT == 1 ? 4 : 2) void attention_dq_kernel(const AttnArgs a) {
   using G = Geo<DP>;
@@ -775,7 +776,8 @@ __device__ __forceinline__ void hide_rows(const AttnArgs& a, int q0, int key, in
 // rows.  They all start where the row tile's number is the same modulo the
 // range's tiles and wrap round at its end, so that work-groups that run
 // together read the same tiles at about the same time (16384 tokens, window
-// 1024, 32 heads of 128 over 8 key heads: dK/dV 582 us, 644 without).
+// 1024, 32 heads of 128 over 8 key heads: dK/dV 622 us, 642 without, and dQ
+// in front of it 451 and 460).
 template <int DP, bool EXACT, int NW, bool WIN>
 struct QueryStream {
   using L = DkvLds<DP>;

@@ -28,7 +28,7 @@ __global__ __launch_bounds__(256, 2) void attention_far_kernel(const AttnArgs a)
   // Every other tile begins a chunk (kFarRows is two tiles): first those at even
   // places of the list, then the others, since work-groups that exit at once
   // between ones that stay leave units without any (16384 tokens, 4 first
-  // tokens, 32/8 heads of 128: 57 us for 89).
+  // tokens, 32/8 heads of 128: 63 us for 100).
   const int place = blockIdx.x / a.kv_heads, evens = (a.n_tiles + 1) / 2;
   const AttnTile t = a.by_query[place < evens ? 2 * place : 2 * (place - evens) + 1];
   const int end = min(t.len, t.first + kFarRows);

@@ -6,8 +6,8 @@
 // Squares of float32 numbers and their sums are formed in float64: a square
 // is exact there (48 bits), none overflows or vanishes, and a norm over 10^9
 // elements keeps its digits.  The vector unit does float64 products at the
-// float32 rate, so memory stays the bound: 307 M float32 values 176 us for the
-// sum (7.0 TB/s), 302 for clipping them into bfloat16 (6.1 TB/s).  Every sum runs in a fixed order
+// float32 rate, so memory stays the bound: 307 M float32 values 180 us for the
+// sum (6.8 TB/s), 302 for clipping them into bfloat16 (6.1 TB/s).  Every sum runs in a fixed order
 // (lane, wave, work-group, partials), so results repeat bit for bit.
 #include "grad_internal.h"
 #include "muon_internal.h"

@@ -114,8 +114,8 @@ muon_status_t check(const Call& c, muon_packing_t packing, const std::vector<Ran
 }
 
 // Whether a lane can hold eight pairs (16-byte accesses) rather than four: 16384
-// tokens, 32/8 heads of 128, forward / gradient 68 / 103 us with eight, 70 / 117 with
-// four; 8192 tokens, 16/2 heads of 80, 15.9 / 25.6 and 15.2 / 30.3.
+// tokens, 32/8 heads of 128, forward / gradient 53 / 107 us with eight, 55 / 125 with
+// four; 8192 tokens, 16/2 heads of 80, 12.9 / 23.2 and 12.4 / 26.5.
 bool is_wide(const muon_qk_rotate_t& a) {
   return a.rotary.rotary_dim % 16 == 0 && (a.head_dim - a.rotary.rotary_dim) % 16 == 0;
 }

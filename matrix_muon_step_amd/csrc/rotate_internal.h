@@ -7,14 +7,16 @@
 namespace muon {
 
 // Tokens of one work item, a piece of a packing's 128-row tile: few enough for
-// many work items, enough to pay for a token's angles.  16384 tokens, 32/8
-// heads of 128, us, forward / gradient: 8 68 / 109, 16 72 / 114; 4100 tokens, 25/25
-// heads of 64 14.3 / 26.8 and 13.8 / 24.2 (2 and 4 were slower in a first form).
+// many work items, enough to pay for a token's angles.  Calls among others, us,
+// forward / gradient: 16384 tokens, 32/8 heads of 128, three axes 8 53 / 107, 16
+// 55 / 116; 16384, 25/25 heads of 64 33 / 57 and 34 / 62; 4100 in ten sequences
+// 11.6 / 24.5 and 12.4 / 22.8 (2 and 4 were slower in a first form).
 constexpr int kRotateRows = 8;
 constexpr int kRotatePieces = kAttnRows / kRotateRows;
 // Work-groups of the backward kernel at most, for each of the two tensors, each
-// with one partial sum of the weight's gradient in the workspace (the 16384
-// tokens: 512 103 us, 1024 109, 2048 112).
+// with one partial sum of the weight's gradient in the workspace (gradient, us,
+// of the 16384 tokens with heads of 128, of 64 and of the 4100: 512 107, 57 and
+// 24.5; 1024 106, 59 and 26.4; 2048 110, 62 and 26.2).
 constexpr int kRotateGroups = 512;
 constexpr int kRotateLanes = 256;
 // Heads of a lane's float32 sums of the weight's gradient at most: with the
@@ -22,8 +24,8 @@ constexpr int kRotateLanes = 256;
 constexpr int kRotateRun = 60;
 // A call whose tensors are more bytes than the memory-side cache holds writes
 // past the caches.  Forward in us, through | past them, with the inputs in the
-// cache and not: 16384 tokens, 32/8 heads of 128 (336 MB) 68 | 52 and 67 | 66; 25/25
-// heads of 64 (210 MB) 33 | 40 and 42.5 | 45.6.  (Reads past them too were slower
+// cache and not: 16384 tokens, 32/8 heads of 128 (336 MB) 71 | 53 and 71 | 68; 25/25
+// heads of 64 (210 MB) 33 | 38 and 47 | 45.  (Reads past them too were slower
 // wherever the cache held the inputs.)
 constexpr int64_t kRotateLarge = int64_t{256} << 20;
 
@@ -58,7 +60,7 @@ struct RotateForm {
   bool wide;         // eight pairs to a lane (rotary_dim and head_dim - rotary_dim multiples of 16), else four
   bool interleaved;
   bool norm;
-  bool large;        // more bytes than the caches hold: reads and writes past them
+  bool large;        // more bytes than the memory-side cache holds: writes past the caches
 };
 // Launches it and, where a weight's gradient is asked for, the kernel that joins its sums.
 hipError_t launch_rotate(const RotateArgs& a, const RotateForm& f, hipStream_t s);
